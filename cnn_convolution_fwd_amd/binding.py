@@ -9,7 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import List, Optional, Sequence, Tuple, Union
+from typing import List, NamedTuple, Optional, Sequence, Tuple, Union
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libcfwd.so")
@@ -18,7 +18,7 @@ LIB_PATH = os.path.join(HERE, "libcfwd.so")
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_NO_CANDIDATE, ERR_HIP, ERR_CACHE_IO = range(7)
 LAYOUT_NCHW, LAYOUT_NCHWX, LAYOUT_NHWC = 0, 1, 2
 _LAYOUTS = {"NCHW": LAYOUT_NCHW, "NCHWX": LAYOUT_NCHWX, "NHWC": LAYOUT_NHWC}
-F32, BF16, I8 = 0, 1, 2
+F32, BF16, I8, MXFP4 = 0, 1, 2, 3
 ALGO_AUTO, ALGO_IMPLICIT_GEMM, ALGO_WINOGRAD_F2X2_3X3, ALGO_WINOGRAD_F6X6_3X3, ALGO_DIRECT, ALGO_POINTWISE = range(6)
 
 ALGO_NAMES = {
@@ -34,8 +34,11 @@ EXPORTED = [
     "cfwd_conv2d_fwd_noalloc", "cfwd_conv2d_fwd_ex", "cfwd_fastrun_allow_inexact_int8",
     "cfwd_bottleneck_check", "cfwd_bottleneck_filter_size", "cfwd_bottleneck_prepare", "cfwd_bottleneck_fwd",
     "cfwd_convert_layout", "cfwd_unpack_int4",
+    "cfwd_mx_size", "cfwd_mx_quantize", "cfwd_mx_dequantize", "cfwd_mx_matmul_workspace_size", "cfwd_mx_matmul",
+    "cfwd_gated_norm",
 ]
-ACT_NONE, ACT_RELU = 0, 1
+ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU = 0, 1, 2, 3
+NORM_NONE, NORM_RMS, NORM_LAYER = 0, 1, 2
 NOALLOC_SCRATCH_BYTES = 64 << 20  # CFWD_NOALLOC_SCRATCH_BYTES
 
 
@@ -60,6 +63,20 @@ class BottleneckEpilogue(ctypes.Structure):
     _fields_ = [("b1", ctypes.c_void_p), ("b2", ctypes.c_void_p), ("b3", ctypes.c_void_p),
                 ("residual", ctypes.c_void_p), ("relu1", ctypes.c_int), ("relu2", ctypes.c_int),
                 ("relu3", ctypes.c_int)]
+
+
+class MxMatmulDesc(ctypes.Structure):
+    """cfwd_mx_matmul_desc: y [m, n] = act(x [m, k] w [n, k]^T + bias)."""
+    _fields_ = [("m", ctypes.c_longlong), ("n", ctypes.c_int), ("k", ctypes.c_int), ("x_dtype", ctypes.c_int),
+                ("y_dtype", ctypes.c_int), ("x_stride", ctypes.c_longlong), ("act", ctypes.c_int)]
+
+
+class GatedNormDesc(ctypes.Structure):
+    """cfwd_gated_norm_desc: s = residual_scale * r + gate * post(b), h = pre(s) over rows of c values."""
+    _fields_ = [("rows", ctypes.c_longlong), ("c", ctypes.c_int), ("rows_per_gate", ctypes.c_longlong),
+                ("residual_scale", ctypes.c_float), ("eps", ctypes.c_float), ("post", ctypes.c_int),
+                ("pre", ctypes.c_int), ("dtype", ctypes.c_int), ("stream_dtype", ctypes.c_int),
+                ("out_dtype", ctypes.c_int)]
 
 
 class Algo(ctypes.Structure):
@@ -121,6 +138,12 @@ def _lib():
             "cfwd_bottleneck_filter_size": [P(BottleneckDesc), P(sz)],
             "cfwd_bottleneck_prepare": [P(BottleneckDesc), vp, vp, sz, vp],
             "cfwd_bottleneck_fwd": [P(BottleneckDesc), vp, vp, vp, vp, P(BottleneckEpilogue), vp, vp],
+            "cfwd_mx_size": [ctypes.c_longlong, ctypes.c_int, P(sz), P(sz)],
+            "cfwd_mx_quantize": [ctypes.c_longlong, ctypes.c_int, ctypes.c_int, vp, ctypes.c_longlong, vp, vp, vp],
+            "cfwd_mx_dequantize": [ctypes.c_longlong, ctypes.c_int, ctypes.c_int, vp, vp, vp, vp],
+            "cfwd_mx_matmul_workspace_size": [P(MxMatmulDesc), P(sz)],
+            "cfwd_mx_matmul": [P(MxMatmulDesc)] + [vp] * 8 + [sz, vp],
+            "cfwd_gated_norm": [P(GatedNormDesc)] + [vp] * 11,
             "cfwd_fastrun_choose": [P(Algo), P(ctypes.c_float), ctypes.c_int, ctypes.c_int, P(ctypes.c_int),
                                     P(ctypes.c_int)],
         }
@@ -586,3 +609,286 @@ def unpack_int4(packed, count: int, out=None):
         out = torch.empty(count, dtype=torch.int8, device=packed.device)
     _check(_lib().cfwd_unpack_int4(packed.data_ptr(), out.data_ptr(), int(count), _stream()))
     return out
+
+
+# ------------------------------------------------------- MXFP4 and the feed-forward block
+
+_ACTS = {"none": ACT_NONE, "relu": ACT_RELU, "silu": ACT_SILU, "gelu": ACT_GELU}
+_NORMS = {"none": NORM_NONE, "rms": NORM_RMS, "layer": NORM_LAYER}
+_MX_CODES = {**{k: v for k, v in _DTYPE_CODES.items() if v != I8}, "mx": MXFP4, "mxfp4": MXFP4}
+
+
+class MxTensor(NamedTuple):
+    """Rows in microscaled 4-bit floating point (format: cfwd.h): ``codes`` uint8 [..., 16 * ceil(cols / 32)],
+    ``scales`` uint8 [..., ceil(cols / 32) rounded up to 4], ``cols`` values a row."""
+    codes: object
+    scales: object
+    cols: int
+
+    @property
+    def shape(self):
+        return (*self.codes.shape[:-1], self.cols)
+
+
+def mx_pitches(cols: int) -> Tuple[int, int]:
+    """Bytes of a row's codes and of its scales."""
+    kb = -(-cols // 32)
+    return 16 * kb, -(-kb // 4) * 4
+
+
+def _code(table, key, what: str) -> int:
+    try:
+        return table[key]
+    except (KeyError, TypeError):
+        raise ValueError("unknown %s %r (one of %s)" % (what, key, ", ".join(sorted(table)))) from None
+
+
+def _float_code(t) -> int:
+    code = _DTYPE_CODES[_dtype_of(t)]
+    if code == I8:
+        raise TypeError("unsupported dtype %s (float32 or bfloat16)" % t.dtype)
+    return code
+
+
+def _rows_of(t) -> Tuple[int, int, int]:
+    """(rows, values a row, row pitch) of a tensor whose last axis is dense and whose rows are evenly spaced."""
+    if t.dim() == 0:
+        raise ValueError("a tensor with at least one axis is needed")
+    k = t.shape[-1]
+    if t.is_contiguous():
+        return (t.numel() // k if k else 0), k, k
+    if t.dim() != 2 or t.stride(1) != 1:
+        try:
+            t = t.view(-1, k)
+        except RuntimeError:
+            raise ValueError("the rows of a tensor of strides %s are not evenly spaced" % (tuple(t.stride()),)) from None
+    if t.shape[0] > 1 and (t.stride(0) < k or (k > 1 and t.stride(1) != 1)) or (k > 1 and t.stride(1) != 1):
+        raise ValueError("rows must be dense and must not overlap")
+    return t.shape[0], k, t.stride(0) if t.shape[0] > 1 else k
+
+
+def _one_device(first, *ts):
+    """All on the GPU that ``first`` is on; all but ``first`` dense."""
+    if not first.is_cuda:
+        raise ValueError("tensors must be on the GPU")
+    for t in ts:
+        if t is None:
+            continue
+        if t.device != first.device:
+            raise ValueError("tensors must be on one GPU")
+        if not t.is_contiguous():
+            raise ValueError("tensors must be contiguous")
+
+
+def _check_mx(t: MxTensor, what: str):
+    torch = _torch()
+    if not isinstance(t, MxTensor):
+        raise TypeError("%s must be an MxTensor" % what)
+    cp, sp = mx_pitches(t.cols)
+    if t.codes.dtype != torch.uint8 or t.scales.dtype != torch.uint8:
+        raise TypeError("%s: codes and scales must be uint8" % what)
+    if t.codes.shape[-1] != cp or tuple(t.scales.shape) != (*t.codes.shape[:-1], sp):
+        raise ValueError("%s: codes %s and scales %s do not hold rows of %d values"
+                         % (what, tuple(t.codes.shape), tuple(t.scales.shape), t.cols))
+
+
+def _enqueue(device, call):
+    """call(stream) on ``device`` and its current stream."""
+    torch = _torch()
+    if device.index == torch.cuda.current_device():
+        _check(call(torch.cuda.current_stream().cuda_stream))
+    else:
+        with torch.cuda.device(device):
+            _check(call(torch.cuda.current_stream().cuda_stream))
+
+
+def _ptr(t) -> Optional[int]:
+    return None if t is None else t.data_ptr()
+
+
+def _new_mx(lead, cols: int, device) -> MxTensor:
+    torch = _torch()
+    cp, sp = mx_pitches(cols)
+    return MxTensor(torch.empty((*lead, cp), dtype=torch.uint8, device=device),
+                    torch.empty((*lead, sp), dtype=torch.uint8, device=device), cols)
+
+
+def _check_mx_out(t: MxTensor, shape):
+    _check_mx(t, "out")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("out must hold %s values" % (tuple(shape),))
+
+
+def mx_quantize(x, out: Optional[MxTensor] = None) -> MxTensor:
+    """x [..., k] (float32 / bfloat16, rows evenly spaced) in MXFP4 (cfwd_mx_quantize)."""
+    rows, k, stride = _rows_of(x)
+    code = _float_code(x)
+    if out is None:
+        _one_device(x)
+        out = _new_mx(x.shape[:-1], k, x.device)
+    else:
+        _check_mx_out(out, x.shape)
+        _one_device(x, out.codes, out.scales)
+    _enqueue(x.device, lambda st: _lib().cfwd_mx_quantize(rows, k, code, x.data_ptr(), stride, out.codes.data_ptr(),
+                                                          out.scales.data_ptr(), st))
+    return out
+
+
+def mx_dequantize(t: MxTensor, dtype="f32", out=None):
+    """The values of an MXFP4 tensor in float32 or bfloat16, both exact (cfwd_mx_dequantize)."""
+    torch = _torch()
+    _check_mx(t, "the tensor")
+    if out is None:
+        code = _code(_MX_CODES, dtype, "dtype")
+        if code == MXFP4:
+            raise ValueError("dtype must be f32 or bf16")
+        out = torch.empty(t.shape, dtype=torch.float32 if code == F32 else torch.bfloat16, device=t.codes.device)
+    elif tuple(out.shape) != tuple(t.shape):
+        raise ValueError("out must have the shape %s" % (tuple(t.shape),))
+    code = _float_code(out)
+    _one_device(t.codes, t.codes, t.scales, out)
+    rows = t.codes.numel() // t.codes.shape[-1]
+    _enqueue(out.device, lambda st: _lib().cfwd_mx_dequantize(rows, t.cols, code, t.codes.data_ptr(),
+                                                              t.scales.data_ptr(), out.data_ptr(), st))
+    return out
+
+
+def mx_matmul_workspace_size(desc: MxMatmulDesc) -> int:
+    b = ctypes.c_size_t()
+    _check(_lib().cfwd_mx_matmul_workspace_size(ctypes.byref(desc), ctypes.byref(b)))
+    return b.value
+
+
+def mx_matmul(x, w: MxTensor, bias=None, act: str = "none", out_dtype=None, out=None, workspace=None):
+    """act(x w^T + bias): x [..., k] against MXFP4 weights [n, k] (cfwd_mx_matmul).
+
+    ``x`` is an MxTensor, or float32 / bfloat16 and then quantised by the call
+    exactly as ``mx_quantize`` does.  A 1x1 convolution of NHWC activations is
+    this product with its channels as the rows.  ``act``: none, relu, silu or
+    gelu (the form with tanh); ``bias`` float32 [n].  ``out_dtype``: f32, bf16
+    or mx (default: x's own, bf16 for an MxTensor).  ``workspace`` (uint8,
+    ``mx_matmul_workspace_size`` bytes) is allocated when not given.
+    """
+    torch = _torch()
+    _check_mx(w, "w")
+    x_mx = isinstance(x, MxTensor)
+    if w.codes.dim() != 2:
+        raise ValueError("w must be a matrix [n, k]")
+    n, k = w.shape
+    if x_mx:
+        _check_mx(x, "x")
+        _one_device(x.codes, x.codes, x.scales, w.codes, w.scales, bias, workspace)
+        rows, stride, x_code, device = x.codes.numel() // x.codes.shape[-1], k, MXFP4, x.codes.device
+    else:
+        _one_device(x, w.codes, w.scales, bias, workspace)
+        rows, _, stride = _rows_of(x)
+        x_code, device = _float_code(x), x.device
+    if x.shape[-1] != k:
+        raise ValueError("x has rows of %d values, w of %d" % (x.shape[-1], k))
+    if bias is not None and (bias.dtype != torch.float32 or tuple(bias.shape) != (n,)):
+        raise ValueError("bias must be float32 [%d]" % n)
+    shape = (*x.shape[:-1], n)
+    if out is not None:
+        if isinstance(out, MxTensor):
+            _check_mx_out(out, shape)
+            y_code = MXFP4
+            _one_device(w.codes, out.codes, out.scales)
+        else:
+            if tuple(out.shape) != shape:
+                raise ValueError("out must have the shape %s" % (shape,))
+            y_code = _float_code(out)
+            _one_device(w.codes, out)
+        if out_dtype is not None and _code(_MX_CODES, out_dtype, "out_dtype") != y_code:
+            raise ValueError("out is not of out_dtype")
+    else:
+        y_code = _code(_MX_CODES, out_dtype, "out_dtype") if out_dtype is not None else BF16 if x_mx else x_code
+        out = _new_mx(shape[:-1], n, device) if y_code == MXFP4 else \
+            torch.empty(shape, dtype=torch.float32 if y_code == F32 else torch.bfloat16, device=device)
+    desc = MxMatmulDesc(rows, n, k, x_code, y_code, stride, _code(_ACTS, act, "act"))
+    ws_bytes = mx_matmul_workspace_size(desc)
+    if workspace is not None:
+        ws_bytes = workspace.numel() * workspace.element_size()
+    elif ws_bytes:
+        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=device)
+    xp, xs = (x.codes.data_ptr(), x.scales.data_ptr()) if x_mx else (x.data_ptr(), None)
+    yp, ys = (out.codes.data_ptr(), out.scales.data_ptr()) if y_code == MXFP4 else (out.data_ptr(), None)
+    _enqueue(device, lambda st: _lib().cfwd_mx_matmul(ctypes.byref(desc), xp, xs, w.codes.data_ptr(),
+                                                      w.scales.data_ptr(), _ptr(bias), yp, ys, _ptr(workspace),
+                                                      ws_bytes, st))
+    return out
+
+
+def gated_norm(b, residual=None, gate=None, residual_scale: float = 1.0, post: str = "none", post_weight=None,
+               post_bias=None, pre: str = "rms", pre_weight=None, pre_bias=None, eps: float = 1e-6, out_dtype=None,
+               sum_out=None, out=None, want_sum: bool = True):
+    """(s, h): s = residual_scale * residual + gate * post(b), h = pre(s) over the last axis (cfwd_gated_norm).
+
+    ``b`` (float32 / bfloat16 [..., c], or None) is a block's output,
+    ``residual`` (b's dtype, or float32) the residual stream.  ``gate``
+    [g, c] or [c] has one row for each run of ceil(rows / g) rows (images,
+    sequences).  ``post`` and ``pre``: none, rms or layer, with float32 [c]
+    weights and biases.  h is in b's dtype, or an MxTensor for ``out_dtype``
+    "mx", ready for ``mx_matmul``; without b and gate it may be float32 or
+    bfloat16 as ``out_dtype`` says; ``pre`` "none" gives h = None.  s is
+    written to ``sum_out`` (which may be ``residual``); ``want_sum`` False: not at all.
+    """
+    torch = _torch()
+    like = b if b is not None else residual
+    if like is None:
+        raise ValueError("b and residual must not both be None")
+    _one_device(like, like, b, residual, gate, post_weight, post_bias, pre_weight, pre_bias, sum_out)
+    if like.dim() == 0:
+        raise ValueError("a tensor with at least one axis is needed")
+    shape, c = tuple(like.shape), like.shape[-1]
+    rows = like.numel() // c if c else 0
+    b_code = _float_code(b if b is not None else gate if gate is not None else like)
+    s_code = _float_code(residual) if residual is not None else _float_code(sum_out) if sum_out is not None else b_code
+    if b is not None and residual is not None and tuple(residual.shape) != shape:
+        raise ValueError("b and residual must have one shape")
+    per = 0
+    if gate is not None:
+        if _float_code(gate) != b_code or gate.dim() not in (1, 2) or gate.shape[-1] != c:
+            raise ValueError("gate must be [groups, %d] of b's dtype" % c)
+        groups = gate.shape[0] if gate.dim() == 2 else 1
+        if groups == 0 and rows:
+            raise ValueError("gate has no rows")
+        per = -(-rows // groups) if groups else 0
+    for name, t in (("post_weight", post_weight), ("post_bias", post_bias), ("pre_weight", pre_weight),
+                    ("pre_bias", pre_bias)):
+        if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != (c,)):
+            raise ValueError("%s must be float32 [%d]" % (name, c))
+    post_code, pre_code = _code(_NORMS, post, "norm"), _code(_NORMS, pre, "norm")
+    h_code = b_code
+    if out is not None:
+        h_code = MXFP4 if isinstance(out, MxTensor) else _float_code(out)
+        if h_code == MXFP4:
+            _check_mx_out(out, shape)
+            _one_device(like, out.codes, out.scales)
+        else:
+            if tuple(out.shape) != shape:
+                raise ValueError("out must have the shape %s" % (shape,))
+            _one_device(like, out)
+    if out_dtype is not None:
+        code = _code(_MX_CODES, out_dtype, "out_dtype")
+        if out is not None and code != h_code:
+            raise ValueError("out is not of out_dtype")
+        h_code = code
+    if b is None and gate is None and h_code != MXFP4:
+        b_code = h_code  # nothing else has b's dtype
+    dt = {F32: torch.float32, BF16: torch.bfloat16}
+    if sum_out is not None:
+        if tuple(sum_out.shape) != shape or _float_code(sum_out) != s_code:
+            raise ValueError("sum_out must have residual's shape and dtype")
+    elif want_sum or pre_code == NORM_NONE:
+        sum_out = torch.empty(shape, dtype=dt[s_code], device=like.device)
+    if pre_code == NORM_NONE:
+        out, h_code = None, b_code
+    elif out is None:
+        out = _new_mx(shape[:-1], c, like.device) if h_code == MXFP4 else \
+            torch.empty(shape, dtype=dt[h_code], device=like.device)
+    desc = GatedNormDesc(rows, c, per, residual_scale, eps, post_code, pre_code, b_code, s_code, h_code)
+    hp, hs = (out.codes.data_ptr(), out.scales.data_ptr()) if isinstance(out, MxTensor) else (_ptr(out), None)
+    _enqueue(like.device, lambda st: _lib().cfwd_gated_norm(
+        ctypes.byref(desc), _ptr(b), _ptr(residual), _ptr(gate), _ptr(post_weight), _ptr(post_bias), _ptr(pre_weight),
+        _ptr(pre_bias), _ptr(sum_out), hp, hs, st))
+    return sum_out, out

@@ -110,7 +110,8 @@ typedef enum {
 
 typedef enum { CFWD_LAYOUT_NCHW = 0, CFWD_LAYOUT_NCHWX = 1, CFWD_LAYOUT_NHWC = 2 } cfwd_layout;
 
-typedef enum { CFWD_F32 = 0, CFWD_BF16 = 1, CFWD_I8 = 2 } cfwd_dtype;
+/* MXFP4: only where the section on 4-bit floating point names it. */
+typedef enum { CFWD_F32 = 0, CFWD_BF16 = 1, CFWD_I8 = 2, CFWD_MXFP4 = 3 } cfwd_dtype;
 
 typedef enum {
     CFWD_ALGO_AUTO = 0,
@@ -141,8 +142,9 @@ typedef struct {
     float median_ms;
 } cfwd_algo;
 
-/* Activation of the fused epilogue. */
-typedef enum { CFWD_ACT_NONE = 0, CFWD_ACT_RELU = 1 } cfwd_activation;
+/* Activation of the fused epilogue.  Convolutions take NONE and RELU; the
+ * MXFP4 product also v / (1 + e^-v) and 0.5 v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))). */
+typedef enum { CFWD_ACT_NONE = 0, CFWD_ACT_RELU = 1, CFWD_ACT_SILU = 2, CFWD_ACT_GELU = 3 } cfwd_activation;
 
 /* Fused epilogue of cfwd_conv2d_fwd_ex: what a ResNet block applies after
  * its convolution, folded into the convolution's own output pass (Momenta
@@ -372,6 +374,89 @@ cfwd_status cfwd_bottleneck_prepare(const cfwd_bottleneck_desc *desc, const void
 cfwd_status cfwd_bottleneck_fwd(const cfwd_bottleneck_desc *desc, const void *x, const void *w1,
                                 const void *w2_prepared, const void *w3,
                                 const cfwd_bottleneck_epilogue *epilogue, void *y, void *stream);
+
+/* ---- Microscaled 4-bit floating point (MXFP4) and the feed-forward block.
+ * For the parts of a network that are products over channels: 1x1
+ * convolutions of NHWC activations, fully connected layers, the feed-forward
+ * halves of transformer layers.  gfx950's matrix cores take MXFP4 operands.
+ *
+ * Format: 32 consecutive values of a row ("block") share a scale.
+ *   codes   uint8 [rows][16 * KB], KB = ceil(k / 32): two values a byte, the
+ *           even one in the low four bits; bit 3 of a value is its sign, bits
+ *           0..2 name 0, 0.5, 1, 1.5, 2, 3, 4, 6 (E2M1).  Values past k are 0.
+ *   scales  uint8 [rows][KB rounded up to a multiple of 4]: 2^(byte - 127),
+ *           255 = NaN; the bytes past KB are 127.
+ * Quantisation of a block: with E the biased fp32 exponent of its largest
+ * magnitude, byte = max(E - 2, 0), or 255 if the block holds a NaN or an
+ * infinity (its codes are then 0); each value / scale is rounded to the
+ * nearest E2M1 value, a tie to the even code, saturating at 6, sign kept.
+ *
+ * codes must be 16-byte aligned, scales 4-byte; x and y in fp32 / bf16
+ * need only their element's alignment, bias and weights 4 bytes.  rows (m)
+ * may be 0: nothing is done.  1 <= k <= 2^22, 1 <= n <= 2^22.  Every call
+ * is enqueued on `stream`, allocates nothing and gives the same bits each time. */
+
+/* Bytes of the codes and of the scales of `rows` rows of k values. */
+cfwd_status cfwd_mx_size(long long rows, int k, size_t *code_bytes, size_t *scale_bytes);
+
+/* x [rows][k] (fp32 / bf16, row pitch x_stride >= k elements) -> codes, scales. */
+cfwd_status cfwd_mx_quantize(long long rows, int k, cfwd_dtype dtype, const void *x, long long x_stride,
+                             void *codes, void *scales, void *stream);
+
+/* The values that codes and scales stand for -> y [rows][k] (fp32 / bf16, both exact). */
+cfwd_status cfwd_mx_dequantize(long long rows, int k, cfwd_dtype dtype, const void *codes, const void *scales,
+                               void *y, void *stream);
+
+/* y [m][n] = act(x w^T + bias): x [m][k], w MXFP4 [n][k]. */
+typedef struct {
+    long long m;
+    int n, k;
+    cfwd_dtype x_dtype; /* MXFP4, or fp32 / bf16: x is quantised by the call, to the same codes as cfwd_mx_quantize's */
+    cfwd_dtype y_dtype; /* fp32, bf16 (round to nearest even) or MXFP4 (quantised from the fp32 result) */
+    long long x_stride; /* row pitch of an fp32 / bf16 x in elements, >= k; ignored for MXFP4 */
+    cfwd_activation act;
+} cfwd_mx_matmul_desc;
+
+/* Workspace bytes of cfwd_mx_matmul (the quantised x, partial sums of a split reduction); 0 when none. */
+cfwd_status cfwd_mx_matmul_workspace_size(const cfwd_mx_matmul_desc *desc, size_t *bytes);
+
+/* The product: exact products, fp32 sums, bias and activation in fp32, one
+ * rounding to y.  x_scales and y_scales belong to an MXFP4 x / y and are NULL
+ * otherwise.  bias: fp32 [n] or NULL.  y and y_scales must not overlap an
+ * input; workspace 256-byte aligned. */
+cfwd_status cfwd_mx_matmul(const cfwd_mx_matmul_desc *desc, const void *x, const void *x_scales, const void *w,
+                           const void *w_scales, const float *bias, void *y, void *y_scales, void *workspace,
+                           size_t ws_bytes, void *stream);
+
+/* Norms before and after a block, with its gate and the residual scale:
+ *   s = residual_scale * r + gate * post(b)      h = pre(s)
+ * b: the block's output, r: the residual stream, s: the new residual stream,
+ * h: the next block's input, all [rows][c].  A norm of v over its row is
+ *   RMS    v / sqrt(mean(v^2) + eps) * weight + bias
+ *   LAYER  (v - mean(v)) / sqrt(mean((v - mean(v))^2) + eps) * weight + bias
+ *   NONE   v
+ * All in fp32; s and h are rounded once, h from the unrounded s. */
+typedef enum { CFWD_NORM_NONE = 0, CFWD_NORM_RMS = 1, CFWD_NORM_LAYER = 2 } cfwd_norm_kind;
+
+typedef struct {
+    long long rows;
+    int c;
+    long long rows_per_gate;  /* row i takes row i / rows_per_gate of gate; 0: one row of gate for all */
+    float residual_scale, eps;
+    cfwd_norm_kind post, pre;
+    cfwd_dtype dtype;         /* of b and gate: fp32 or bf16 */
+    cfwd_dtype stream_dtype;  /* of r and s: fp32, or bf16 where dtype is bf16 */
+    cfwd_dtype out_dtype;     /* of h: dtype, or MXFP4 */
+} cfwd_gated_norm_desc;
+
+/* b or residual may be NULL (it then contributes 0), gate NULL (1), s or h
+ * NULL (not wanted); weights and biases are fp32 [c] or NULL (1 and 0).
+ * gate: [ceil(rows / rows_per_gate)][c].  h_scales: with an MXFP4 h only.  s
+ * may be residual itself, or b itself where both have one type; apart from that no output
+ * may overlap an input or the other output.  1 <= c <= 2^22, eps >= 0. */
+cfwd_status cfwd_gated_norm(const cfwd_gated_norm_desc *desc, const void *b, const void *residual, const void *gate,
+                            const float *post_weight, const float *post_bias, const float *pre_weight,
+                            const float *pre_bias, void *s, void *h, void *h_scales, void *stream);
 
 /* Static description of a status code. */
 const char *cfwd_status_string(cfwd_status status);
