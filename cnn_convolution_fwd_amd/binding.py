@@ -652,54 +652,60 @@ def _float_code(t) -> int:
 
 def _rows_of(t) -> Tuple[int, int, int]:
     """(rows, values a row, row pitch) of a tensor whose last axis is dense and whose rows are evenly spaced."""
-    if t.dim() == 0:
+    shape = t.shape
+    if not shape:
         raise ValueError("a tensor with at least one axis is needed")
-    k = t.shape[-1]
+    k = shape[-1]
     if t.is_contiguous():
         return (t.numel() // k if k else 0), k, k
-    if t.dim() != 2 or t.stride(1) != 1:
+    if len(shape) != 2:
         try:
             t = t.view(-1, k)
         except RuntimeError:
-            raise ValueError("the rows of a tensor of strides %s are not evenly spaced" % (tuple(t.stride()),)) from None
-    if t.shape[0] > 1 and (t.stride(0) < k or (k > 1 and t.stride(1) != 1)) or (k > 1 and t.stride(1) != 1):
+            raise ValueError("the rows of a tensor of strides %s are not evenly spaced" % (t.stride(),)) from None
+    rows, stride = t.shape[0], t.stride(0)
+    if (k > 1 and t.stride(1) != 1) or (rows > 1 and stride < k):
         raise ValueError("rows must be dense and must not overlap")
-    return t.shape[0], k, t.stride(0) if t.shape[0] > 1 else k
+    return rows, k, stride if rows > 1 else k
 
 
-def _one_device(first, *ts):
-    """All on the GPU that ``first`` is on; all but ``first`` dense."""
-    if not first.is_cuda:
+def _check_on(dev: int, *ts):
+    """Every tensor that is given is on GPU ``dev`` (-1: the first one was on none) and dense."""
+    if dev < 0:
         raise ValueError("tensors must be on the GPU")
     for t in ts:
-        if t is None:
-            continue
-        if t.device != first.device:
-            raise ValueError("tensors must be on one GPU")
-        if not t.is_contiguous():
-            raise ValueError("tensors must be contiguous")
+        if t is not None:
+            if t.get_device() != dev:
+                raise ValueError("tensors must be on one GPU")
+            if not t.is_contiguous():
+                raise ValueError("tensors must be contiguous")
 
 
-def _check_mx(t: MxTensor, what: str):
-    torch = _torch()
+def _check_mx(t: MxTensor, what: str) -> int:
+    """Rows of an MxTensor whose parts fit each other."""
     if not isinstance(t, MxTensor):
         raise TypeError("%s must be an MxTensor" % what)
-    cp, sp = mx_pitches(t.cols)
-    if t.codes.dtype != torch.uint8 or t.scales.dtype != torch.uint8:
+    codes, scales, cols = t
+    u8 = _torch().uint8
+    if codes.dtype != u8 or scales.dtype != u8:
         raise TypeError("%s: codes and scales must be uint8" % what)
-    if t.codes.shape[-1] != cp or tuple(t.scales.shape) != (*t.codes.shape[:-1], sp):
+    cs, ss = codes.shape, scales.shape
+    cp, sp = mx_pitches(cols)
+    if not cp or cs[-1] != cp or ss[-1] != sp or cs[:-1] != ss[:-1]:
         raise ValueError("%s: codes %s and scales %s do not hold rows of %d values"
-                         % (what, tuple(t.codes.shape), tuple(t.scales.shape), t.cols))
+                         % (what, tuple(cs), tuple(ss), cols))
+    return codes.numel() // cp
 
 
-def _enqueue(device, call):
-    """call(stream) on ``device`` and its current stream."""
+def _guard(dev: int):
+    """None when ``dev`` is the current GPU, else a context that makes it that (kernels go to the current GPU's stream)."""
     torch = _torch()
-    if device.index == torch.cuda.current_device():
-        _check(call(torch.cuda.current_stream().cuda_stream))
-    else:
-        with torch.cuda.device(device):
-            _check(call(torch.cuda.current_stream().cuda_stream))
+    return None if dev == torch.cuda.current_device() else torch.cuda.device(dev)
+
+
+def _stream_of(dev: int) -> int:
+    """Handle of the current stream of GPU ``dev``; the plain call behind torch.cuda.current_stream, 2.7 us cheaper."""
+    return _torch()._C._cuda_getCurrentRawStream(dev)
 
 
 def _ptr(t) -> Optional[int]:
@@ -721,23 +727,29 @@ def _check_mx_out(t: MxTensor, shape):
 
 def mx_quantize(x, out: Optional[MxTensor] = None) -> MxTensor:
     """x [..., k] (float32 / bfloat16, rows evenly spaced) in MXFP4 (cfwd_mx_quantize)."""
+    dev = x.get_device()
     rows, k, stride = _rows_of(x)
     code = _float_code(x)
     if out is None:
-        _one_device(x)
+        _check_on(dev)
         out = _new_mx(x.shape[:-1], k, x.device)
     else:
         _check_mx_out(out, x.shape)
-        _one_device(x, out.codes, out.scales)
-    _enqueue(x.device, lambda st: _lib().cfwd_mx_quantize(rows, k, code, x.data_ptr(), stride, out.codes.data_ptr(),
-                                                          out.scales.data_ptr(), st))
+        _check_on(dev, out.codes, out.scales)
+    guard = _guard(dev)
+    if guard is not None:
+        with guard:
+            return mx_quantize(x, out)
+    _check(_lib().cfwd_mx_quantize(rows, k, code, x.data_ptr(), stride, out.codes.data_ptr(), out.scales.data_ptr(),
+                                   _stream_of(dev)))
     return out
 
 
 def mx_dequantize(t: MxTensor, dtype="f32", out=None):
     """The values of an MXFP4 tensor in float32 or bfloat16, both exact (cfwd_mx_dequantize)."""
     torch = _torch()
-    _check_mx(t, "the tensor")
+    rows = _check_mx(t, "the tensor")
+    dev = t.codes.get_device()
     if out is None:
         code = _code(_MX_CODES, dtype, "dtype")
         if code == MXFP4:
@@ -745,11 +757,15 @@ def mx_dequantize(t: MxTensor, dtype="f32", out=None):
         out = torch.empty(t.shape, dtype=torch.float32 if code == F32 else torch.bfloat16, device=t.codes.device)
     elif tuple(out.shape) != tuple(t.shape):
         raise ValueError("out must have the shape %s" % (tuple(t.shape),))
-    code = _float_code(out)
-    _one_device(t.codes, t.codes, t.scales, out)
-    rows = t.codes.numel() // t.codes.shape[-1]
-    _enqueue(out.device, lambda st: _lib().cfwd_mx_dequantize(rows, t.cols, code, t.codes.data_ptr(),
-                                                              t.scales.data_ptr(), out.data_ptr(), st))
+    else:
+        code = _float_code(out)
+    _check_on(dev, t.codes, t.scales, out)
+    guard = _guard(dev)
+    if guard is not None:
+        with guard:
+            return mx_dequantize(t, out=out)
+    _check(_lib().cfwd_mx_dequantize(rows, t.cols, code, t.codes.data_ptr(), t.scales.data_ptr(), out.data_ptr(),
+                                     _stream_of(dev)))
     return out
 
 
@@ -770,51 +786,60 @@ def mx_matmul(x, w: MxTensor, bias=None, act: str = "none", out_dtype=None, out=
     ``mx_matmul_workspace_size`` bytes) is allocated when not given.
     """
     torch = _torch()
-    _check_mx(w, "w")
-    x_mx = isinstance(x, MxTensor)
-    if w.codes.dim() != 2:
+    n = _check_mx(w, "w")
+    w_codes, w_scales, k = w
+    if w_codes.dim() != 2:
         raise ValueError("w must be a matrix [n, k]")
-    n, k = w.shape
-    if x_mx:
-        _check_mx(x, "x")
-        _one_device(x.codes, x.codes, x.scales, w.codes, w.scales, bias, workspace)
-        rows, stride, x_code, device = x.codes.numel() // x.codes.shape[-1], k, MXFP4, x.codes.device
+    if isinstance(x, MxTensor):
+        rows, stride, x_code = _check_mx(x, "x"), k, MXFP4
+        xt, x_scales, x_k = x
+        lead, dev = xt.shape[:-1], xt.get_device()
+        _check_on(dev, xt, x_scales, w_codes, w_scales, bias, workspace)
+        xs = x_scales.data_ptr()
     else:
-        _one_device(x, w.codes, w.scales, bias, workspace)
-        rows, _, stride = _rows_of(x)
-        x_code, device = _float_code(x), x.device
-    if x.shape[-1] != k:
-        raise ValueError("x has rows of %d values, w of %d" % (x.shape[-1], k))
-    if bias is not None and (bias.dtype != torch.float32 or tuple(bias.shape) != (n,)):
+        xt, xs = x, None
+        rows, x_k, stride = _rows_of(x)
+        x_code, lead, dev = _float_code(x), x.shape[:-1], x.get_device()
+        _check_on(dev, w_codes, w_scales, bias, workspace)
+    if x_k != k:
+        raise ValueError("x has rows of %d values, w of %d" % (x_k, k))
+    if bias is not None and (bias.dtype != torch.float32 or bias.shape != (n,)):
         raise ValueError("bias must be float32 [%d]" % n)
-    shape = (*x.shape[:-1], n)
-    if out is not None:
-        if isinstance(out, MxTensor):
-            _check_mx_out(out, shape)
-            y_code = MXFP4
-            _one_device(w.codes, out.codes, out.scales)
-        else:
-            if tuple(out.shape) != shape:
-                raise ValueError("out must have the shape %s" % (shape,))
-            y_code = _float_code(out)
-            _one_device(w.codes, out)
-        if out_dtype is not None and _code(_MX_CODES, out_dtype, "out_dtype") != y_code:
-            raise ValueError("out is not of out_dtype")
+    y_code = _code(_MX_CODES, out_dtype, "out_dtype") if out_dtype is not None else None
+    if out is None:
+        if y_code is None:
+            y_code = BF16 if x_code == MXFP4 else x_code
+        out = _new_mx(lead, n, xt.device) if y_code == MXFP4 else torch.empty(
+            (*lead, n), dtype=torch.float32 if y_code == F32 else torch.bfloat16, device=xt.device)
     else:
-        y_code = _code(_MX_CODES, out_dtype, "out_dtype") if out_dtype is not None else BF16 if x_mx else x_code
-        out = _new_mx(shape[:-1], n, device) if y_code == MXFP4 else \
-            torch.empty(shape, dtype=torch.float32 if y_code == F32 else torch.bfloat16, device=device)
-    desc = MxMatmulDesc(rows, n, k, x_code, y_code, stride, _code(_ACTS, act, "act"))
-    ws_bytes = mx_matmul_workspace_size(desc)
+        if isinstance(out, MxTensor):
+            _check_mx_out(out, (*lead, n))
+            code = MXFP4
+            _check_on(dev, out.codes, out.scales)
+        else:
+            if tuple(out.shape) != (*lead, n):
+                raise ValueError("out must have the shape %s" % ((*lead, n),))
+            code = _float_code(out)
+            _check_on(dev, out)
+        if y_code is not None and y_code != code:
+            raise ValueError("out is not of out_dtype")
+        y_code = code
+    act_code = _code(_ACTS, act, "act")
+    guard = _guard(dev)
+    if guard is not None:
+        with guard:
+            return mx_matmul(x, w, bias, act, None, out, workspace)
+    desc = MxMatmulDesc(rows, n, k, x_code, y_code, stride, act_code)
     if workspace is not None:
-        ws_bytes = workspace.numel() * workspace.element_size()
-    elif ws_bytes:
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=device)
-    xp, xs = (x.codes.data_ptr(), x.scales.data_ptr()) if x_mx else (x.data_ptr(), None)
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    else:
+        ws, ws_bytes = None, mx_matmul_workspace_size(desc)
+        if ws_bytes:
+            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=xt.device)
+            ws = workspace.data_ptr()
     yp, ys = (out.codes.data_ptr(), out.scales.data_ptr()) if y_code == MXFP4 else (out.data_ptr(), None)
-    _enqueue(device, lambda st: _lib().cfwd_mx_matmul(ctypes.byref(desc), xp, xs, w.codes.data_ptr(),
-                                                      w.scales.data_ptr(), _ptr(bias), yp, ys, _ptr(workspace),
-                                                      ws_bytes, st))
+    _check(_lib().cfwd_mx_matmul(ctypes.byref(desc), xt.data_ptr(), xs, w_codes.data_ptr(), w_scales.data_ptr(),
+                                 _ptr(bias), yp, ys, ws, ws_bytes, _stream_of(dev)))
     return out
 
 
@@ -836,15 +861,17 @@ def gated_norm(b, residual=None, gate=None, residual_scale: float = 1.0, post: s
     like = b if b is not None else residual
     if like is None:
         raise ValueError("b and residual must not both be None")
-    _one_device(like, like, b, residual, gate, post_weight, post_bias, pre_weight, pre_bias, sum_out)
-    if like.dim() == 0:
+    dev, shape = like.get_device(), like.shape
+    if not shape:
         raise ValueError("a tensor with at least one axis is needed")
-    shape, c = tuple(like.shape), like.shape[-1]
+    _check_on(dev, b, residual, gate, post_weight, post_bias, pre_weight, pre_bias, sum_out)
+    c = shape[-1]
     rows = like.numel() // c if c else 0
-    b_code = _float_code(b if b is not None else gate if gate is not None else like)
-    s_code = _float_code(residual) if residual is not None else _float_code(sum_out) if sum_out is not None else b_code
-    if b is not None and residual is not None and tuple(residual.shape) != shape:
+    if b is not None and residual is not None and residual.shape != shape:
         raise ValueError("b and residual must have one shape")
+    b_code = _float_code(b if b is not None else gate if gate is not None else like)
+    stream_like = residual if residual is not None else sum_out
+    s_code = b_code if stream_like is None else _float_code(stream_like)
     per = 0
     if gate is not None:
         if _float_code(gate) != b_code or gate.dim() not in (1, 2) or gate.shape[-1] != c:
@@ -855,40 +882,42 @@ def gated_norm(b, residual=None, gate=None, residual_scale: float = 1.0, post: s
         per = -(-rows // groups) if groups else 0
     for name, t in (("post_weight", post_weight), ("post_bias", post_bias), ("pre_weight", pre_weight),
                     ("pre_bias", pre_bias)):
-        if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != (c,)):
+        if t is not None and (t.dtype != torch.float32 or t.shape != (c,)):
             raise ValueError("%s must be float32 [%d]" % (name, c))
     post_code, pre_code = _code(_NORMS, post, "norm"), _code(_NORMS, pre, "norm")
-    h_code = b_code
+    h_code = b_code if out_dtype is None else _code(_MX_CODES, out_dtype, "out_dtype")
     if out is not None:
-        h_code = MXFP4 if isinstance(out, MxTensor) else _float_code(out)
-        if h_code == MXFP4:
-            _check_mx_out(out, shape)
-            _one_device(like, out.codes, out.scales)
-        else:
-            if tuple(out.shape) != shape:
-                raise ValueError("out must have the shape %s" % (shape,))
-            _one_device(like, out)
-    if out_dtype is not None:
-        code = _code(_MX_CODES, out_dtype, "out_dtype")
-        if out is not None and code != h_code:
+        code = MXFP4 if isinstance(out, MxTensor) else _float_code(out)
+        if out_dtype is not None and code != h_code:
             raise ValueError("out is not of out_dtype")
         h_code = code
+        if code == MXFP4:
+            _check_mx_out(out, shape)
+            _check_on(dev, out.codes, out.scales)
+        else:
+            if out.shape != shape:
+                raise ValueError("out must have the shape %s" % (tuple(shape),))
+            _check_on(dev, out)
     if b is None and gate is None and h_code != MXFP4:
         b_code = h_code  # nothing else has b's dtype
-    dt = {F32: torch.float32, BF16: torch.bfloat16}
     if sum_out is not None:
-        if tuple(sum_out.shape) != shape or _float_code(sum_out) != s_code:
+        if sum_out.shape != shape or _float_code(sum_out) != s_code:
             raise ValueError("sum_out must have residual's shape and dtype")
     elif want_sum or pre_code == NORM_NONE:
-        sum_out = torch.empty(shape, dtype=dt[s_code], device=like.device)
+        sum_out = torch.empty_like(stream_like if stream_like is not None else like)
     if pre_code == NORM_NONE:
         out, h_code = None, b_code
     elif out is None:
         out = _new_mx(shape[:-1], c, like.device) if h_code == MXFP4 else \
-            torch.empty(shape, dtype=dt[h_code], device=like.device)
+            torch.empty(shape, dtype=torch.float32 if h_code == F32 else torch.bfloat16, device=like.device)
+    guard = _guard(dev)
+    if guard is not None:
+        with guard:
+            return gated_norm(b, residual, gate, residual_scale, post, post_weight, post_bias, pre, pre_weight,
+                              pre_bias, eps, out_dtype, sum_out, out, want_sum)
     desc = GatedNormDesc(rows, c, per, residual_scale, eps, post_code, pre_code, b_code, s_code, h_code)
-    hp, hs = (out.codes.data_ptr(), out.scales.data_ptr()) if isinstance(out, MxTensor) else (_ptr(out), None)
-    _enqueue(like.device, lambda st: _lib().cfwd_gated_norm(
-        ctypes.byref(desc), _ptr(b), _ptr(residual), _ptr(gate), _ptr(post_weight), _ptr(post_bias), _ptr(pre_weight),
-        _ptr(pre_bias), _ptr(sum_out), hp, hs, st))
+    hp, hs = (out.codes.data_ptr(), out.scales.data_ptr()) if h_code == MXFP4 else (_ptr(out), None)
+    _check(_lib().cfwd_gated_norm(ctypes.byref(desc), _ptr(b), _ptr(residual), _ptr(gate), _ptr(post_weight),
+                                  _ptr(post_bias), _ptr(pre_weight), _ptr(pre_bias), _ptr(sum_out), hp, hs,
+                                  _stream_of(dev)))
     return sum_out, out

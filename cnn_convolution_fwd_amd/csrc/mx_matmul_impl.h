@@ -14,6 +14,8 @@
 
 #include "mx.h"
 
+#include <type_traits>
+
 namespace cfwd {
 namespace mx {
 
@@ -21,7 +23,9 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 struct MatmulParams {
-    const uint8_t *x, *xs, *w, *ws;
+    const uint8_t *x, *xs, *w, *ws;  // x: codes, or (stream kernel) values of x_stride elements a row
+    long long x_stride;
+    int k;
     const float* bias;
     void* y;
     uint8_t* ys;
@@ -153,4 +157,10 @@ __device__ __forceinline__ void write_rows(const f32x16 (&acc)[FN], const Matmul
 }
 
 }  // namespace mx
+
+// Few rows (k_mx_stream.hip).  `x`: MXFP4, or x's own type where mx_stream_takes_raw says so.
+bool mx_stream_supported(long long m);
+bool mx_stream_takes_raw(long long m, int k);
+cfwd_status mx_stream(const mx::MatmulParams& p, cfwd_dtype x, cfwd_dtype y, hipStream_t st);
+
 }  // namespace cfwd
