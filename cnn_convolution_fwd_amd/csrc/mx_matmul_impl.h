@@ -20,6 +20,7 @@ namespace cfwd {
 namespace mx {
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 struct MatmulParams {
@@ -50,110 +51,180 @@ __device__ __forceinline__ f32x16 mfma(const i32x4& a, const i32x4& b, const f32
     return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a8, b8, c, 4, 4, J, sa, J, sb);
 }
 
-// The output pass of one wave's 32 rows of y x 32 FN columns: bias,
-// activation, rounding, and a turn through the wave's own LDS area so that
-// whole runs of columns are stored.  TY: float, bf16_t, or void for MXFP4.
-template <int FN, typename TY>
-constexpr int out_area() {  // bytes of the wave's LDS area
-    return std::is_void<TY>::value ? 32 * (FN * 16 + 16) + 32 * FN
-                                   : 32 * (FN * 32 * (std::is_same<TY, float>::value ? 4 : 2) + 16);
+// The output pass of one wave: 32 FM rows of y x 32 FN columns from (m0, n0)
+// on, with bias (add_bias(f, v) adds that of columns' fragment f), activation
+// and the one rounding.
+//
+// fp32 and bf16 results take a turn through the wave's own LDS area (32 rows of
+// AREA_ROW bytes, 16-byte slots permuted by row instead of padded), so that
+// whole runs of columns are stored.  An MXFP4 block (32 columns of a row) is
+// spread over the two lanes r and r + 32, which exchange halves of two blocks,
+// so that each then holds a block's 16 bytes.
+//
+// `fast`: rows of y are whole 16-byte runs, which leave as buffer stores,
+// out-of-range ones dropped by the hardware: each wave then issues exactly
+// stores<FM, FN, TY>() of them.  Otherwise stores follow the row's ends.
+template <int FM, int FN, typename TY>
+constexpr int stores() {
+    return std::is_void<TY>::value ? FM * FN : FM * FN * (std::is_same<TY, float>::value ? 4 : 2);
 }
 
-template <int FN, typename TY>
-__device__ __forceinline__ void write_rows(const f32x16 (&acc)[FN], const MatmulParams& p, long long m0, int n0,
-                                           uint8_t* area) {
-    const int lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5;
-    const __amdgpu_buffer_rsrc_t bias = buffer(p.bias, p.bias ? p.n * 4ll : 0);
-    if constexpr (!std::is_void<TY>::value) {
-        constexpr int ES = sizeof(TY), PITCH = FN * 32 * ES + 16;
+__device__ __forceinline__ void activate16(float (&v)[16], int act) {
+    if (act == CFWD_ACT_NONE) return;
+    if (act == CFWD_ACT_RELU) {
 #pragma unroll
-        for (int f = 0; f < FN; ++f)
+        for (int i = 0; i < 16; ++i) v[i] = activate(v[i], CFWD_ACT_RELU);
+    } else if (act == CFWD_ACT_SILU) {
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const int c = f * 32 + g * 8 + h * 4;
-                const i32x4 q = __builtin_bit_cast(
-                    i32x4, __builtin_amdgcn_raw_buffer_load_b128(bias, (n0 + c) * 4, 0, 0));
-                float v[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] = activate(acc[f][g * 4 + i] + __int_as_float(q[i]), p.act);
-                if constexpr (ES == 4)
-                    *reinterpret_cast<float4*>(area + r * PITCH + c * 4) = make_float4(v[0], v[1], v[2], v[3]);
-                else
-                    *reinterpret_cast<uint2*>(area + r * PITCH + c * 2) =
-                        make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
-            }
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        constexpr int RUN = 16 / ES, RUNS = FN * 32 / RUN;  // 16-byte runs of a row
-#pragma unroll
-        for (int i = 0; i < RUNS / 2; ++i) {
-            const int u = i * 64 + lane, row = u / RUNS, c = u % RUNS * RUN;
-            const Raw16 t = *reinterpret_cast<const Raw16*>(__builtin_assume_aligned(area + row * PITCH + c * ES, 16));
-            const long long m = m0 + row;
-            const int valid = p.n - (n0 + c);
-            if (m >= p.m || valid <= 0) continue;
-            TY* dst = static_cast<TY*>(p.y) + m * p.n + n0 + c;
-            if (valid >= RUN) {
-                *reinterpret_cast<Raw16*>(dst) = t;
-            } else {
-#pragma unroll
-                for (int j = 0; j < RUN; ++j)
-                    if (j < valid) {
-                        if constexpr (ES == 4)
-                            dst[j] = __uint_as_float(t.w[j]);
-                        else
-                            dst[j].bits = static_cast<uint16_t>(t.w[j / 2] >> (j % 2 * 16));
-                    }
-            }
-        }
+        for (int i = 0; i < 16; ++i) v[i] = activate(v[i], CFWD_ACT_SILU);
     } else {
-        constexpr int PITCH = FN * 16 + 16;
-        uint8_t* sarea = area + 32 * PITCH;
 #pragma unroll
-        for (int f = 0; f < FN; ++f) {
-            const int nb = n0 + f * 32;
-            float v[16];
-            uint32_t top = 0;
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const int n = nb + g * 8 + h * 4;
-                const i32x4 q =
-                    __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(bias, n * 4, 0, 0));
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float t = activate(acc[f][g * 4 + i] + __int_as_float(q[i]), p.act);
-                    v[g * 4 + i] = n + i < p.n ? t : 0.0f;  // a column past the row is no part of its block
-                    top = max(top, abs_bits(v[g * 4 + i]));
-                }
-            }
-            top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 32)));
-            const uint32_t byte = nb < p.n ? exponent_byte(top) : 127u;
-            const float s = scale_of(byte);
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                uint32_t c = 0;
-                c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[g * 4], v[g * 4 + 1], s, 0);
-                c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[g * 4 + 2], v[g * 4 + 3], s, 1);
-                *reinterpret_cast<uint16_t*>(area + r * PITCH + f * 16 + g * 4 + h * 2) =
-                    byte == 255 ? 0 : static_cast<uint16_t>(c);
-            }
-            if (h == 0) sarea[r * FN + f] = static_cast<uint8_t>(byte);
-        }
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-#pragma unroll
-        for (int i = 0; i < (FN + 1) / 2; ++i) {  // one block of one row a lane
-            const int u = i * 64 + lane, row = u / FN, f = u % FN;
-            const long long m = m0 + row;
-            if (u < 32 * FN && m < p.m && n0 + f * 32 < p.n)
-                *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.y) + m * p.y_pitch + (n0 / 32 + f) * 16) =
-                    *reinterpret_cast<const uint4*>(area + row * PITCH + f * 16);
-            if (u < 32 * FN && m < p.m && n0 / 32 + f < p.y_spitch)
-                p.ys[m * p.y_spitch + n0 / 32 + f] = sarea[row * FN + f];
-        }
+        for (int i = 0; i < 16; ++i) v[i] = activate(v[i], CFWD_ACT_GELU);
     }
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();  // the area is written again only after every lane has read it
+}
+
+__device__ __forceinline__ void wave_sync() {  // a wave's LDS writes before its later reads, and the reverse
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_sched_barrier(0);  // and no register holds more than one turn's results
+}
+
+// bias of a lane's 16 columns of the 32 from n on
+__device__ __forceinline__ void load_bias(const MatmulParams& p, int n, float (&v)[16]) {
+    const __amdgpu_buffer_rsrc_t b = buffer(p.bias, p.n * 4ll);
+    const int h = (threadIdx.x >> 5) & 1;
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+        const u32x4 q = __builtin_amdgcn_raw_buffer_load_b128(b, (n + g * 8 + h * 4) * 4, 0, 0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[g * 4 + i] = __uint_as_float(q[i]);
+    }
+}
+
+template <int FM, int FN, typename TY, typename Bias>
+__device__ __forceinline__ void write_tile(const f32x16 (&acc)[FM][FN], Bias add_bias, const MatmulParams& p,
+                                           long long m0, int n0, bool fast, uint8_t* area) {
+    int lane = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane));  // keeps the pass's many addresses from being computed, and held, outside the caller's loop
+    const int r = lane & 31, h = lane >> 5;
+    const long long rows = min(32ll * FM, p.m - m0);
+    if constexpr (!std::is_void<TY>::value) {
+        constexpr int ES = sizeof(TY), CF = ES == 4 ? FN / 2 : FN;  // columns' fragments of one turn
+        constexpr int ROW = CF * 32 * ES, SLOTS = ROW / 16, RUN = 16 / ES;
+        const long long pitch = static_cast<long long>(p.n) * ES;
+        uint8_t* y0 = static_cast<uint8_t*>(p.y) + m0 * pitch + static_cast<long long>(n0) * ES;
+        const __amdgpu_buffer_rsrc_t y = buffer(y0, (rows - 1) * pitch + (static_cast<long long>(p.n) - n0) * ES);
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int f0 = 0; f0 < FN; f0 += CF) {
+#pragma unroll
+                for (int f = 0; f < CF; ++f) {
+                    float v[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) v[j] = acc[i][f0 + f][j];
+                    add_bias(f0 + f, v);
+                    activate16(v, p.act);
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        const int byte = (f * 32 + g * 8 + h * 4) * ES;
+                        uint8_t* at = area + r * ROW + ((byte / 16) ^ (r & (SLOTS - 1))) * 16 + byte % 16;
+                        if constexpr (ES == 4)
+                            *reinterpret_cast<float4*>(at) = make_float4(v[g * 4], v[g * 4 + 1], v[g * 4 + 2], v[g * 4 + 3]);
+                        else
+                            *reinterpret_cast<uint2*>(at) =
+                                make_uint2(pack_bf16x2(v[g * 4], v[g * 4 + 1]), pack_bf16x2(v[g * 4 + 2], v[g * 4 + 3]));
+                    }
+                }
+                wave_sync();
+                constexpr int STEP = 64 / SLOTS;  // rows of one access of the wave
+                const int row0 = lane / SLOTS, slot = lane % SLOTS, c = f0 * 32 + slot * RUN, valid = p.n - n0 - c;
+                auto run = [&](int u) {
+                    const int row = u * STEP + row0;
+                    return *reinterpret_cast<const u32x4*>(area + row * ROW + (slot ^ (row & (SLOTS - 1))) * 16);
+                };
+                if (fast) {
+                    const uint32_t off = valid > 0 ? row0 * static_cast<uint32_t>(pitch) + c * ES : kOutOfRange;
+#pragma unroll
+                    for (int u = 0; u < SLOTS / 2; ++u)
+                        __builtin_amdgcn_raw_buffer_store_b128(
+                            run(u), y, off + (i * 32 + u * STEP) * static_cast<uint32_t>(pitch), 0, 0);
+                } else {
+#pragma nounroll
+                    for (int u = 0; u < SLOTS / 2; ++u) {
+                        const u32x4 t = run(u);
+                        const int row = i * 32 + u * STEP + row0;
+                        if (row >= rows || valid <= 0) continue;
+                        TY* dst = reinterpret_cast<TY*>(y0 + row * pitch) + c;
+                        if (valid >= RUN) {
+                            *reinterpret_cast<Raw16*>(dst) = Raw16{{t[0], t[1], t[2], t[3]}};
+                            continue;
+                        }
+#pragma unroll
+                        for (int j = 0; j < RUN; ++j)
+                            if (j < valid) {
+                                if constexpr (ES == 4)
+                                    dst[j] = __uint_as_float(t[j]);
+                                else
+                                    dst[j].bits = static_cast<uint16_t>(t[j / 2] >> (j % 2 * 16));
+                            }
+                    }
+                }
+                wave_sync();
+            }
+    } else {
+        const __amdgpu_buffer_rsrc_t y = buffer(static_cast<uint8_t*>(p.y) + m0 * p.y_pitch, rows * p.y_pitch),
+                                     ys = buffer(p.ys + m0 * p.y_spitch, rows * p.y_spitch);
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int f0 = 0; f0 < FN; f0 += 2) {
+                uint32_t half[2][2], byte[2];  // this lane's halves of two blocks: codes of g = 0, 1 and of g = 2, 3
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const int nb = n0 + (f0 + q) * 32;
+                    float v[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) v[j] = acc[i][f0 + q][j];
+                    add_bias(f0 + q, v);
+                    activate16(v, p.act);
+                    if (nb + 32 > p.n) {  // columns past the row are no part of its last block
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) v[j] = nb + j / 4 * 8 + h * 4 + j % 4 < p.n ? v[j] : 0.0f;
+                    }
+                    uint32_t top = 0;
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) top = max(top, abs_bits(v[j]));
+                    top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 32)));
+                    byte[q] = nb < p.n ? exponent_byte(top) : 127u;
+                    const float s = scale_of(byte[q]);
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        uint32_t c = 0;
+                        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[t * 8], v[t * 8 + 1], s, 0);
+                        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[t * 8 + 2], v[t * 8 + 3], s, 1);
+                        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[t * 8 + 4], v[t * 8 + 5], s, 2);
+                        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[t * 8 + 6], v[t * 8 + 7], s, 3);
+                        half[q][t] = byte[q] == 255 ? 0u : c;
+                    }
+                }
+                // lanes of half 0 take block f0, those of half 1 block f0 + 1
+                u32x4 block;
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    const auto x = __builtin_amdgcn_permlane32_swap(half[0][t], half[1][t], false, false);
+                    block[2 * t] = __builtin_amdgcn_perm(x[1], x[0], 0x05040100u);
+                    block[2 * t + 1] = __builtin_amdgcn_perm(x[1], x[0], 0x07060302u);
+                }
+                __builtin_amdgcn_sched_barrier(0);  // no register holds more than one turn's results
+                const int nb = n0 / 32 + f0 + h;    // rows past the end are out of the buffers' range
+                const uint32_t off = nb * 16 < p.y_pitch ? r * p.y_pitch + nb * 16 : kOutOfRange;
+                const uint32_t soff = nb < p.y_spitch ? r * p.y_spitch + nb : kOutOfRange;
+                __builtin_amdgcn_raw_buffer_store_b128(block, y, off + i * 32 * p.y_pitch, 0, 0);
+                __builtin_amdgcn_raw_buffer_store_b8(static_cast<uint8_t>(h ? byte[1] : byte[0]), ys,
+                                                     soff + i * 32 * p.y_spitch, 0, 0);
+            }
+    }
 }
 
 }  // namespace mx
