@@ -2,7 +2,7 @@
 #include "mx_matmul_impl.h"
 
 #include <algorithm>
-#include <cstdlib>
+#include <atomic>
 #include <type_traits>
 
 namespace cfwd {
@@ -51,15 +51,22 @@ __device__ __forceinline__ void barrier() { asm volatile("s_barrier" ::: "memory
 // (8192^3: 368 us so, 306 us without any scale copies).
 //
 // A stage's row is 64 bytes, four blocks, of which half h of a wave takes
-// blocks 2 h and 2 h + 1; block b of row i lies in slot b ^ ((i >> 1) & 3), so
-// that the 16-byte reads of consecutive rows spread over all banks.  The copy
-// to LDS is linear in lanes, so the permutation is made in the addresses that
-// the lanes load from.
+// blocks 2 h and 2 h + 1.  LDS serves 16 lanes' 16 bytes at once if they cover
+// its 64 banks, four rows, so block b of row i lies in slot b ^ ((i >> 2) & 3):
+// 16 rows' reads of one block then do.  The copy to LDS is linear in lanes, so
+// the permutation is made in the addresses that the lanes load from.
 //
 // The output pass of the tile uses the LDS of the stage multiplied last, which
 // is filled again only after the next stage's barrier.
+struct Tiling {
+    int tiles_m, tiles_n;
+    int splits, split_stages;  // parts of the sum over K, each with its own y (m x ldy) behind the last; stages of a part
+    Divisor tiles;             // of one part
+    Divisor group, height, last_height;  // of tiles in a group of 8 rows of tiles; of rows in a group, in the last one
+};
+
 template <int F, typename TY>
-__global__ __launch_bounds__(256, F > 2 ? 1 : 2) void tile_kernel(MatmulParams p, int tiles_m, int tiles_n, bool fast) {
+__global__ __launch_bounds__(256, F > 2 ? 1 : 2) void tile_kernel(MatmulParams p, Tiling order, bool fast) {
     static_assert(F == 2 || F == 4, "the copies below are laid out for these");
     constexpr int B = 64 * F, STAGE = 2 * B * 64, GROUP = 2 * B * 16;
     constexpr int CODE_LOADS = 2 * F, SCALE_LOADS = 2 * F;  // a wave's copies for a stage, for a group
@@ -71,37 +78,44 @@ __global__ __launch_bounds__(256, F > 2 ? 1 : 2) void tile_kernel(MatmulParams p
 
     // The i-th tile of this workgroup.  A round of tiles is a run of the tiles'
     // order, each XCD a run within it; the order goes down columns of 8 tiles.
-    const int tiles = tiles_m * tiles_n;
+    const int tiles = order.tiles.d * order.splits;
     const int rounds = F > 2 ? 1 : (tiles - 1 - static_cast<int>(blockIdx.x)) / static_cast<int>(gridDim.x) + 1;
-    auto tile_at = [&](int i, long long* m0, int* n0) {
+    auto tile_at = [&](int i, long long* m0, int* n0, int* split) {
         const int first = i * gridDim.x;
-        const int t = first + xcd_linear(blockIdx.x, min(static_cast<int>(gridDim.x), tiles - first));
-        const int group = t / (8 * tiles_n), in_group = t % (8 * tiles_n), height = min(8, tiles_m - group * 8);
-        *m0 = static_cast<long long>(group * 8 + in_group % height) * B;
-        *n0 = in_group / height * B;
+        const int u = first + xcd_linear(blockIdx.x, min(static_cast<int>(gridDim.x), tiles - first));
+        *split = divide(u, order.tiles);
+        const int t = u - *split * order.tiles.d;
+        const int group = divide(t, order.group), in_group = t - group * order.group.d;
+        const Divisor height = group == (order.tiles_m - 1) / 8 ? order.last_height : order.height;
+        const int column = divide(in_group, height);
+        *m0 = static_cast<long long>(group * 8 + in_group - column * height.d) * B;
+        *n0 = column * B;
     };
 
-    const int stages = (p.kb + 3) / 4;
+    const int all_stages = (p.kb + 3) / 4;
+    auto stages_of = [&](int split) { return min(order.split_stages, all_stages - split * order.split_stages); };
     const uint32_t lds0 = static_cast<uint32_t>(
         reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t*)lds));
-    // copying: tile number, stage of the tile, stage and group of all
-    int copy_tile = 0, copy_stage = 0, copy_count = 0, copy_group = 0;
+    // copying: tile number, stage of K and the tile's end, stage and group of all
+    int copy_tile = 0, copy_stage = 0, copy_end = 0, copy_count = 0, copy_group = 0;
     __amdgpu_buffer_rsrc_t gx, gxs, gw, gws;
     auto open_tile = [&] {
         long long m0 = 0, rows_x = 0, rows_w = 0;
-        int n0 = 0;
+        int n0 = 0, split = 0;
         if (copy_tile < rounds) {
-            tile_at(copy_tile, &m0, &n0);
+            tile_at(copy_tile, &m0, &n0, &split);
             rows_x = min(static_cast<long long>(B), p.m - m0);
             rows_w = min(B, p.n - n0);
         }
+        copy_stage = split * order.split_stages;  // a whole number of groups
+        copy_end = copy_stage + stages_of(split);
         gx = buffer(p.x + m0 * p.pitch, rows_x * p.pitch);
         gxs = buffer(p.xs + m0 * p.spitch, rows_x * p.spitch);
         gw = buffer(p.w + static_cast<long long>(n0) * p.pitch, rows_w * p.pitch);
         gws = buffer(p.ws + static_cast<long long>(n0) * p.spitch, rows_w * p.spitch);
     };
     // one copy: 16 rows' codes of a stage, or 16 rows' scales of a group
-    const int copy_block = (lane & 3) ^ ((lane >> 3) & 3);
+    const int copy_block = (lane & 3) ^ (lane >> 4);
     const uint32_t copy_off = (wave * 16 + (lane >> 2)) * p.pitch + copy_block * 16;
     const uint32_t copy_soff = (wave * 16 + (lane >> 2)) * p.spitch + (lane & 3) * 4;
     auto copy_codes = [&](int i) {  // i-th of each operand's F copies
@@ -121,9 +135,8 @@ __global__ __launch_bounds__(256, F > 2 ? 1 : 2) void tile_kernel(MatmulParams p
     };
     auto next_copy = [&] {
         ++copy_count;
-        if ((++copy_stage & 3) == 0 || copy_stage == stages) ++copy_group;
-        if (copy_stage == stages) {
-            copy_stage = 0;
+        if ((++copy_stage & 3) == 0 || copy_stage == copy_end) ++copy_group;
+        if (copy_stage == copy_end) {
             ++copy_tile;
             open_tile();
         }
@@ -132,7 +145,7 @@ __global__ __launch_bounds__(256, F > 2 ? 1 : 2) void tile_kernel(MatmulParams p
     // fragments of one matrix instruction's depth, two sets in turn; scale words of a stage
     i32x4 a[2][F], b[2][F];
     int sw[2][F], sx[2][F];
-    const int swz = (r >> 1) & 3;
+    const int swz = (r >> 2) & 3;
     const uint8_t* lw = lds + (wn * 32 * F + r) * 64;
     const uint8_t* lx = lds + (B + wm * 32 * F + r) * 64;
     const uint8_t* lws = lds + 4 * STAGE + (wn * 32 * F + r) * 16;
@@ -168,11 +181,12 @@ __global__ __launch_bounds__(256, F > 2 ? 1 : 2) void tile_kernel(MatmulParams p
 
     f32x16 acc[F][F] = {};
     int count = 0, group = 0;  // of the stage that is multiplied, among all
-    int since = 2;             // stages since the last output pass
+    int since = 4;             // stages since the last output pass
     for (int tile = 0; tile < rounds; ++tile) {
         long long m0;
-        int n0;
-        tile_at(tile, &m0, &n0);
+        int n0, split;
+        tile_at(tile, &m0, &n0, &split);
+        const int stages = stages_of(split);
         m0 += wm * 32 * F;
         n0 += wn * 32 * F;
         float bias[F > 2 ? 1 : F][16];
@@ -182,7 +196,7 @@ __global__ __launch_bounds__(256, F > 2 ? 1 : 2) void tile_kernel(MatmulParams p
                 for (int f = 0; f < F; ++f) load_bias(p, n0 + f * 32, bias[f]);
             }
         for (int stage = 0; stage < stages; ++stage, ++count, ++since) {
-            // This wave's copies for the next stage: later ones, and stores, may be outstanding.
+            // This wave's copies for the next stage: those for the one after it, and stores, may be outstanding.
             if (since < 2) {
                 if (had_scales) wait_loads<(CODE_LOADS + SCALE_LOADS + STORES < 63 ? CODE_LOADS + SCALE_LOADS + STORES : 63)>();
                 else wait_loads<(CODE_LOADS + STORES < 63 ? CODE_LOADS + STORES : 63)>();
@@ -230,7 +244,10 @@ __global__ __launch_bounds__(256, F > 2 ? 1 : 2) void tile_kernel(MatmulParams p
 #pragma unroll
             for (int j = 0; j < 16; ++j) v[j] += bias[F > 2 ? 0 : f][j];
         };
-        write_tile<F, F, TY>(acc, add_bias, p, m0, n0, fast, lds + ((count - 1) & 3) * STAGE + wave * (STAGE / 4));
+        MatmulParams part = p;
+        if constexpr (std::is_same<TY, float>::value) part.y = static_cast<float*>(p.y) + split * p.m * p.ldy;
+        write_tile<F, F, TY, false>(acc, add_bias, part, m0, n0, fast,
+                                    lds + ((count - 1) & 3) * STAGE + wave * (STAGE / 4), [] {});
         if (!fast) wait_loads<0>();  // an unknown number of stores
 #pragma unroll
         for (int i = 0; i < F; ++i)
@@ -241,45 +258,153 @@ __global__ __launch_bounds__(256, F > 2 ? 1 : 2) void tile_kernel(MatmulParams p
     wait_loads<0>();  // no copy may reach LDS after the workgroup has ended
 }
 
+// The parts of a split sum, one behind the other -> y.  A thread owns 8 columns.
+template <typename TY>
+__global__ __launch_bounds__(256) void join_kernel(MatmulParams p, const float* __restrict__ parts, int splits,
+                                                   Divisor per_row, uint32_t units) {
+    const uint32_t u = blockIdx.x * 256u + threadIdx.x;
+    if (u >= units) return;  // for MXFP4 units is a multiple of 4: whole blocks leave
+    const uint32_t row = divide(u, per_row);
+    const int n = static_cast<int>(u - row * per_row.d) * 8, valid = p.n - n;
+    const float* at = parts + static_cast<long long>(row) * p.ldy + n;
+    float v[8], t[8];
+    load8(at, valid, v);
+    for (int q = 1; q < splits; ++q) {
+        load8(at + q * p.m * p.ldy, valid, t);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] += t[i];
+    }
+    if (p.bias) {
+        load8(p.bias + n, valid, t);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] += t[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = activate(v[i], p.act);
+    store_run<TY>(p, row, n, valid, v);
+}
+
 template <int F>
-void launch_tiles(const MatmulParams& p, cfwd_dtype y, int cus, hipStream_t st) {
+void launch_tiles(const MatmulParams& p, cfwd_dtype y, int splits, int cus, hipStream_t st) {
     const int tiles_m = static_cast<int>((p.m + 64 * F - 1) / (64 * F)), tiles_n = (p.n + 64 * F - 1) / (64 * F);
-    const unsigned grid = static_cast<unsigned>(F > 2 || tiles_m * tiles_n < 2 * cus ? tiles_m * tiles_n : 2 * cus);
+    const int stages = (p.kb + 3) / 4, split_stages = splits > 1 ? (stages + 4 * splits - 1) / (4 * splits) * 4 : stages;
+    const int parts = (stages + split_stages - 1) / split_stages;
+    const Tiling order{tiles_m, tiles_n, parts, split_stages, divisor(tiles_m * tiles_n), divisor(8u * tiles_n),
+                       divisor(8), divisor((tiles_m - 1) % 8 + 1)};
+    const int tiles = tiles_m * tiles_n * parts, slots = 2 * cus;
+    const unsigned grid = static_cast<unsigned>(F > 2 || tiles < slots ? tiles : slots);
     // whole 16-byte runs, and a wave's rows within a buffer's 31 bits
     const int es = y == CFWD_F32 ? 4 : 2;
-    const bool fast = y == CFWD_MXFP4 || (p.n * es % 16 == 0 && reinterpret_cast<uintptr_t>(p.y) % 16 == 0 && p.n <= (1 << 21));
+    const bool fast = y == CFWD_MXFP4 || (p.ldy * es % 16 == 0 && reinterpret_cast<uintptr_t>(p.y) % 16 == 0 && p.n <= (1 << 21));
     if (y == CFWD_F32)
-        tile_kernel<F, float><<<grid, 256, 0, st>>>(p, tiles_m, tiles_n, fast);
+        tile_kernel<F, float><<<grid, 256, 0, st>>>(p, order, fast);
     else if (y == CFWD_BF16)
-        tile_kernel<F, bf16_t><<<grid, 256, 0, st>>>(p, tiles_m, tiles_n, fast);
+        tile_kernel<F, bf16_t><<<grid, 256, 0, st>>>(p, order, fast);
     else
-        tile_kernel<F, void><<<grid, 256, 0, st>>>(p, tiles_m, tiles_n, fast);
+        tile_kernel<F, void><<<grid, 256, 0, st>>>(p, order, fast);
+}
+
+// A split sum: parts in fp32 to `work`, then the joining pass.
+void launch_split(const MatmulParams& p, cfwd_dtype y, int splits, int cus, float* work, hipStream_t st) {
+    const int stages = (p.kb + 3) / 4, split_stages = (stages + 4 * splits - 1) / (4 * splits) * 4;
+    const int parts = (stages + split_stages - 1) / split_stages;
+    MatmulParams q = p;
+    q.bias = nullptr;
+    q.act = CFWD_ACT_NONE;
+    q.y = work;
+    q.ldy = (p.n + 3) / 4 * 4;
+    launch_tiles<2>(q, CFWD_F32, splits, cus, st);
+    q = p;
+    q.ldy = (p.n + 3) / 4 * 4;
+    const Divisor per_row = divisor(y == CFWD_MXFP4 ? p.y_pitch / 4 : (p.n + 7) / 8);
+    const uint32_t units = static_cast<uint32_t>(p.m) * per_row.d, grid = (units + 255) / 256;
+    if (y == CFWD_F32)
+        join_kernel<float><<<grid, 256, 0, st>>>(q, work, parts, per_row, units);
+    else if (y == CFWD_BF16)
+        join_kernel<bf16_t><<<grid, 256, 0, st>>>(q, work, parts, per_row, units);
+    else
+        join_kernel<void><<<grid, 256, 0, st>>>(q, work, parts, per_row, units);
 }
 
 }  // namespace mx
 
 namespace {
+
 size_t round256(size_t v) { return (v + 255) / 256 * 256; }
+
+int compute_units() {  // of the current device; asked for once
+    static std::atomic<int> known[64];
+    int dev = 0, n = 0;
+    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 256;
+    if (int k = known[dev].load(std::memory_order_relaxed)) return k;
+    if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n <= 0) return 256;
+    known[dev].store(n, std::memory_order_relaxed);
+    return n;
+}
+
+// How a product of more rows than the stream kernel takes is cut up: F of the
+// tile kernel, and parts of the sum over K.
+struct Choice {
+    int f, splits;
+};
+
+// The cheapest by a model of the time, in us, fitted to measurements over sums
+// of 4 to 128 stages and 8 to 6000 tiles (n, m = 128 .. 100352), which it meets
+// to about 20%: a round of tiles takes its stages and an output pass; 128-wide
+// tiles share a CU by twos, or run twice as fast alone (8192 x 8192 x 8192: 405
+// us with F = 2, 305 with F = 4; x 1024: 75 and 76; 25088 x 512 x 256: 13 and
+// 16).  A split sum pays for its parts' traffic and a second launch (128 x 1024
+// x 16384: 48 us whole, 19 in 8 parts; 500 x 4096 x 4096: 17 and 26 in 2).
+Choice choose(const cfwd_mx_matmul_desc* d, int cus) {
+    const double stages = static_cast<double>((mx_blocks(d->k) + 3) / 4);
+    const long long t2 = (d->m + 127) / 128 * ((d->n + 127) / 128), t4 = (d->m + 255) / 256 * ((d->n + 255) / 256);
+    auto rounds = [](long long tiles, long long slots) { return static_cast<double>((tiles + slots - 1) / slots); };
+    const double alone = 0.36, shared = 0.74, wide = 1.05;  // us a stage
+    double best = t2 <= cus ? stages * alone + 2 : rounds(t2, 2 * cus) * (stages * shared + 3.4);
+    Choice c{2, 1};
+    const double four = rounds(t4, cus) * (stages * wide + 10);
+    if (four < best) {
+        best = four;
+        c = {4, 1};
+    }
+    for (int s = 2; s <= 8 && t2 * s <= cus && stages >= 4 * s; s *= 2) {
+        const double split = stages / s * alone + 2 + 4 + static_cast<double>(d->m) * d->n * 8 * s / 4e6;
+        if (split < best) {
+            best = split;
+            c = {2, s};
+        }
+    }
+    return c;
+}
+
+size_t x_bytes(const cfwd_mx_matmul_desc* d) {  // of an x that the call quantises
+    return round256(static_cast<size_t>(d->m) * mx_code_pitch(d->k)) + round256(static_cast<size_t>(d->m) * mx_scale_pitch(d->k));
+}
+
 }  // namespace
 
 size_t mx_matmul_workspace(const cfwd_mx_matmul_desc* d) {
-    if (d->x_dtype == CFWD_MXFP4 || (mx_stream_supported(d->m) && mx_stream_takes_raw(d->m, d->k))) return 0;
-    return round256(static_cast<size_t>(d->m) * mx_code_pitch(d->k)) + round256(static_cast<size_t>(d->m) * mx_scale_pitch(d->k));
+    const bool stream = mx_stream_supported(d->m, d->n, d->k);
+    const size_t x = d->x_dtype == CFWD_MXFP4 || (stream && mx_stream_takes_raw(d->m, d->k)) ? 0 : x_bytes(d);
+    if (stream) return x;
+    const Choice c = choose(d, compute_units());
+    return x + (c.splits > 1 ? static_cast<size_t>(c.splits) * d->m * ((d->n + 3) / 4 * 4) * 4 : 0);
 }
 
 cfwd_status mx_matmul(const cfwd_mx_matmul_desc* d, const void* x, const void* x_scales, const void* w,
                       const void* w_scales, const float* bias, void* y, void* y_scales, void* workspace,
                       hipStream_t st) {
     mx::MatmulParams p{};
-    const bool stream = mx_stream_supported(d->m);
+    uint8_t* work = static_cast<uint8_t*>(workspace);
+    const bool stream = mx_stream_supported(d->m, d->n, d->k);
     const bool raw = d->x_dtype != CFWD_MXFP4 && stream && mx_stream_takes_raw(d->m, d->k);
     if (d->x_dtype != CFWD_MXFP4 && !raw) {
-        uint8_t* codes = static_cast<uint8_t*>(workspace);
-        uint8_t* scales = codes + round256(static_cast<size_t>(d->m) * mx_code_pitch(d->k));
-        const cfwd_status s = mx_quantize(d->m, d->k, d->x_dtype, x, d->x_stride, codes, scales, st);
+        uint8_t* scales = work + round256(static_cast<size_t>(d->m) * mx_code_pitch(d->k));
+        const cfwd_status s = mx_quantize(d->m, d->k, d->x_dtype, x, d->x_stride, work, scales, st);
         if (s != CFWD_OK) return s;
-        x = codes;
+        x = work;
         x_scales = scales;
+        work += x_bytes(d);
     }
     p.x = static_cast<const uint8_t*>(x);
     p.xs = static_cast<const uint8_t*>(x_scales);
@@ -290,6 +415,7 @@ cfwd_status mx_matmul(const cfwd_mx_matmul_desc* d, const void* x, const void* x
     p.ys = static_cast<uint8_t*>(y_scales);
     p.m = d->m;
     p.n = d->n;
+    p.ldy = d->n;
     p.kb = static_cast<int>(mx_blocks(d->k));
     p.pitch = static_cast<int>(mx_code_pitch(d->k));
     p.spitch = static_cast<int>(mx_scale_pitch(d->k));
@@ -299,12 +425,14 @@ cfwd_status mx_matmul(const cfwd_mx_matmul_desc* d, const void* x, const void* x
     p.y_pitch = static_cast<int>(mx_code_pitch(d->n));
     p.y_spitch = static_cast<int>(mx_scale_pitch(d->n));
     if (stream) return mx_stream(p, raw ? d->x_dtype : CFWD_MXFP4, d->y_dtype, st);
-    const int cus = 256;
-    const char* force = getenv("MXT");
-    if (force ? atoi(force) == 44 : ((d->m + 255) / 256 * ((d->n + 255) / 256) >= 256))
-        mx::launch_tiles<4>(p, d->y_dtype, cus, st);
+    const int cus = compute_units();
+    const Choice c = choose(d, cus);
+    if (c.splits > 1)
+        mx::launch_split(p, d->y_dtype, c.splits, cus, reinterpret_cast<float*>(work), st);
+    else if (c.f == 4)
+        mx::launch_tiles<4>(p, d->y_dtype, 1, cus, st);
     else
-        mx::launch_tiles<2>(p, d->y_dtype, cus, st);
+        mx::launch_tiles<2>(p, d->y_dtype, 1, cus, st);
     return check_hip(hipGetLastError(), "MXFP4 product launch");
 }
 

@@ -11,23 +11,6 @@
 namespace cfwd {
 namespace mx {
 
-// Division of n < 2^31 by a fixed d as a multiply-high and a shift (the
-// round-up reciprocal, exact for all such n).
-struct Divisor {
-    uint32_t mul, shift, d;
-};
-
-inline Divisor divisor(uint32_t d) {
-    Divisor r{0, 0, d};
-    while ((1ull << r.shift) < d) ++r.shift;
-    r.mul = static_cast<uint32_t>(((1ull << (31 + r.shift)) + d - 1) / d);
-    return r;
-}
-
-__device__ __forceinline__ uint32_t divide(uint32_t n, const Divisor& v) {
-    return static_cast<uint32_t>((static_cast<uint64_t>(n) * v.mul) >> (31 + v.shift));
-}
-
 // unit = (row, 8 values of it); `units` of them, quads of a row's padding included
 template <typename T>
 __global__ __launch_bounds__(256) void quantize_kernel(const T* __restrict__ x, long long x_stride, int k,

@@ -128,24 +128,7 @@ __global__ __launch_bounds__(64 * kWaves) void stream_kernel(MatmulParams p) {
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = activate(v[i], p.act);
-        if constexpr (!std::is_void<TY>::value) {
-            if (valid > 0) store8(static_cast<TY*>(p.y) + static_cast<long long>(row) * p.n + n, valid, v);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = i < valid ? v[i] : 0.0f;
-            uint32_t byte;
-            const uint32_t codes = quantize8(v, &byte);  // RUNS is a multiple of 4: a block's quad runs together
-            const int nb = n / 32;
-            if (nb * 16 < p.y_pitch) {
-                *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.y) + static_cast<long long>(row) * p.y_pitch + n / 2) = codes;
-                if (c % 32 == 0) {
-                    uint8_t* s = p.ys + static_cast<long long>(row) * p.y_spitch;
-                    s[nb] = static_cast<uint8_t>(byte);
-                    if ((nb + 1) * 16 == p.y_pitch)
-                        for (int i = nb + 1; i < p.y_spitch; ++i) s[i] = 127;
-                }
-            }
-        }
+        store_run<TY>(p, row, n, valid, v);  // RUNS is a multiple of 4 for MXFP4: a block's quad runs together
     }
 }
 
@@ -177,7 +160,12 @@ void launch_stream_n(const MatmulParams& p, cfwd_dtype y, hipStream_t st) {
 // that costs more than one more launch.
 bool mx_stream_takes_raw(long long m, int k) { return m <= 16 && mx_blocks(k) <= 4 * 4 * mx::kWaves; }
 
-bool mx_stream_supported(long long m) { return m <= 64; }
+// Beyond 32 rows every workgroup's reading of x counts: the tile kernel then
+// wins unless w is small (48 rows: 4096 x 4096 10.6 us here, 13.4 there; 11000 x
+// 3000 13.8 and 13.1; 4096 x 16384 33 and 22).
+bool mx_stream_supported(long long m, int n, int k) {
+    return m <= 32 || (m <= 64 && static_cast<long long>(n) * k <= 1 << 24);
+}
 
 cfwd_status mx_stream(const mx::MatmulParams& p, cfwd_dtype x, cfwd_dtype y, hipStream_t st) {
     if (x == CFWD_F32)

@@ -39,6 +39,23 @@ cfwd_status mx_matmul(const cfwd_mx_matmul_desc* d, const void* x, const void* x
 #if defined(__HIPCC__)
 namespace mx {
 
+// Division of n < 2^31 by a fixed d as a multiply-high and a shift (the
+// round-up reciprocal, exact for all such n).
+struct Divisor {
+    uint32_t mul, shift, d;
+};
+
+inline Divisor divisor(uint32_t d) {
+    Divisor r{0, 0, d};
+    while ((1ull << r.shift) < d) ++r.shift;
+    r.mul = static_cast<uint32_t>(((1ull << (31 + r.shift)) + d - 1) / d);
+    return r;
+}
+
+__device__ __forceinline__ uint32_t divide(uint32_t n, const Divisor& v) {
+    return static_cast<uint32_t>((static_cast<uint64_t>(n) * v.mul) >> (31 + v.shift));
+}
+
 // 16 and 8 bytes at any address that suits the element type: the compiler
 // uses whole loads and stores, which the hardware splits where it must.
 struct __attribute__((packed, aligned(2))) Raw16 {

@@ -6,10 +6,10 @@
 // bytes) of row lane % 32 of each, with the block's scale byte, and ends with
 // 16 outputs of one row of y: columns 8 g + 4 h + i (g, i < 4) of 32.
 //
-// A K step ("stage") is 256 values, 8 blocks, as four such instructions.  The
-// order of the sum is free as long as both operands agree, so half h takes
-// the stage's blocks 4 h .. 4 h + 3, one an instruction: their four scale
-// bytes are then one aligned word, and each instruction names its byte.
+// A stage is 256 values of K, 8 blocks, as four such instructions.  The order
+// of the sum is free as long as both operands agree, so half h takes the
+// stage's blocks 4 h .. 4 h + 3, one an instruction: their four scale bytes are
+// then one aligned word, and each instruction names its byte.
 #pragma once
 
 #include "mx.h"
@@ -34,6 +34,7 @@ struct MatmulParams {
     int n, kb;  // kb: blocks of a row
     int pitch, spitch;  // bytes of a row of codes / scales of x and w
     int act;
+    int ldy;                // row pitch of an fp32 / bf16 y, in elements
     int y_pitch, y_spitch;  // MXFP4 outputs
 };
 
@@ -51,15 +52,39 @@ __device__ __forceinline__ f32x16 mfma(const i32x4& a, const i32x4& b, const f32
     return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a8, b8, c, 4, 4, J, sa, J, sb);
 }
 
+// 8 finished values of y's row from column n on, `valid` of them columns of y.
+// An MXFP4 block's four runs belong to a quad of lanes, which all call this.
+template <typename TY>
+__device__ __forceinline__ void store_run(const MatmulParams& p, long long row, int n, int valid, float (&v)[8]) {
+    if constexpr (!std::is_void<TY>::value) {
+        if (valid > 0) store8(static_cast<TY*>(p.y) + row * p.n + n, valid, v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = i < valid ? v[i] : 0.0f;
+        uint32_t byte;
+        const uint32_t codes = quantize8(v, &byte);
+        const int block = n / 32;
+        if (block * 16 >= p.y_pitch) return;
+        *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.y) + row * p.y_pitch + n / 2) = codes;
+        if (n % 32) return;
+        uint8_t* s = p.ys + row * p.y_spitch;
+        s[block] = static_cast<uint8_t>(byte);
+        if ((block + 1) * 16 == p.y_pitch)  // the last block also writes what rounds the row up to whole words
+            for (int i = block + 1; i < p.y_spitch; ++i) s[i] = 127;
+    }
+}
+
 // The output pass of one wave: 32 FM rows of y x 32 FN columns from (m0, n0)
 // on, with bias (add_bias(f, v) adds that of columns' fragment f), activation
 // and the one rounding.
 //
-// fp32 and bf16 results take a turn through the wave's own LDS area (32 rows of
-// AREA_ROW bytes, 16-byte slots permuted by row instead of padded), so that
-// whole runs of columns are stored.  An MXFP4 block (32 columns of a row) is
-// spread over the two lanes r and r + 32, which exchange halves of two blocks,
-// so that each then holds a block's 16 bytes.
+// fp32 and bf16 results take a turn through the wave's own LDS area (32 rows x
+// TURN bytes, 16-byte slots permuted by row instead of padded), so that whole
+// runs of columns are stored.  HOLD: all runs are held in registers,
+// before_stores() is called when the wave is done with LDS, and then they are
+// stored; otherwise each turn's as it comes.  An MXFP4 block (32 columns of a
+// row) is spread over the two lanes r and r + 32, which exchange halves of two
+// blocks, so that each then holds a block's 16 bytes.
 //
 // `fast`: rows of y are whole 16-byte runs, which leave as buffer stores,
 // out-of-range ones dropped by the hardware: each wave then issues exactly
@@ -101,9 +126,9 @@ __device__ __forceinline__ void load_bias(const MatmulParams& p, int n, float (&
     }
 }
 
-template <int FM, int FN, typename TY, typename Bias>
+template <int FM, int FN, typename TY, bool HOLD, typename Bias, typename Before>
 __device__ __forceinline__ void write_tile(const f32x16 (&acc)[FM][FN], Bias add_bias, const MatmulParams& p,
-                                           long long m0, int n0, bool fast, uint8_t* area) {
+                                           long long m0, int n0, bool fast, uint8_t* area, Before before_stores) {
     int lane = threadIdx.x & 63;
     asm volatile("" : "+v"(lane));  // keeps the pass's many addresses from being computed, and held, outside the caller's loop
     const int r = lane & 31, h = lane >> 5;
@@ -111,9 +136,41 @@ __device__ __forceinline__ void write_tile(const f32x16 (&acc)[FM][FN], Bias add
     if constexpr (!std::is_void<TY>::value) {
         constexpr int ES = sizeof(TY), CF = ES == 4 ? FN / 2 : FN;  // columns' fragments of one turn
         constexpr int ROW = CF * 32 * ES, SLOTS = ROW / 16, RUN = 16 / ES;
-        const long long pitch = static_cast<long long>(p.n) * ES;
+        constexpr int TURNS = FM * FN / CF, RUNS = SLOTS / 2, STEP = 64 / SLOTS;  // runs of a lane; rows of one access of the wave
+        const long long pitch = static_cast<long long>(p.ldy) * ES;
         uint8_t* y0 = static_cast<uint8_t*>(p.y) + m0 * pitch + static_cast<long long>(n0) * ES;
-        const __amdgpu_buffer_rsrc_t y = buffer(y0, (rows - 1) * pitch + (static_cast<long long>(p.n) - n0) * ES);
+        const __amdgpu_buffer_rsrc_t y = buffer(y0, (rows - 1) * pitch + (static_cast<long long>(p.ldy) - n0) * ES);
+        const int row0 = lane / SLOTS, slot = lane % SLOTS;
+        auto place = [](int row, int at) { return at ^ ((SLOTS > 8 ? row : row >> 1) & (SLOTS - 1)); };
+        u32x4 held[HOLD ? TURNS : 1][RUNS];
+        auto store_turn = [&](int i, int f0, const u32x4(&t)[RUNS]) {
+            const int c = f0 * 32 + slot * RUN, valid = p.n - n0 - c;
+            if (fast) {
+                const uint32_t off = valid > 0 ? row0 * static_cast<uint32_t>(pitch) + c * ES : kOutOfRange;
+#pragma unroll
+                for (int u = 0; u < RUNS; ++u)
+                    __builtin_amdgcn_raw_buffer_store_b128(t[u], y, off + (i * 32 + u * STEP) * static_cast<uint32_t>(pitch), 0, 0);
+                return;
+            }
+#pragma unroll
+            for (int u = 0; u < RUNS; ++u) {
+                const int row = i * 32 + u * STEP + row0;
+                if (row >= rows || valid <= 0) continue;
+                TY* dst = reinterpret_cast<TY*>(y0 + row * pitch) + c;
+                if (valid >= RUN) {
+                    *reinterpret_cast<Raw16*>(dst) = Raw16{{t[u][0], t[u][1], t[u][2], t[u][3]}};
+                    continue;
+                }
+#pragma unroll
+                for (int j = 0; j < RUN; ++j)
+                    if (j < valid) {
+                        if constexpr (ES == 4)
+                            dst[j] = __uint_as_float(t[u][j]);
+                        else
+                            dst[j].bits = static_cast<uint16_t>(t[u][j / 2] >> (j % 2 * 16));
+                    }
+            }
+        };
 #pragma unroll
         for (int i = 0; i < FM; ++i)
 #pragma unroll
@@ -128,7 +185,7 @@ __device__ __forceinline__ void write_tile(const f32x16 (&acc)[FM][FN], Bias add
 #pragma unroll
                     for (int g = 0; g < 4; ++g) {
                         const int byte = (f * 32 + g * 8 + h * 4) * ES;
-                        uint8_t* at = area + r * ROW + ((byte / 16) ^ (r & (SLOTS - 1))) * 16 + byte % 16;
+                        uint8_t* at = area + r * ROW + place(r, byte / 16) * 16 + byte % 16;
                         if constexpr (ES == 4)
                             *reinterpret_cast<float4*>(at) = make_float4(v[g * 4], v[g * 4 + 1], v[g * 4 + 2], v[g * 4 + 3]);
                         else
@@ -137,42 +194,23 @@ __device__ __forceinline__ void write_tile(const f32x16 (&acc)[FM][FN], Bias add
                     }
                 }
                 wave_sync();
-                constexpr int STEP = 64 / SLOTS;  // rows of one access of the wave
-                const int row0 = lane / SLOTS, slot = lane % SLOTS, c = f0 * 32 + slot * RUN, valid = p.n - n0 - c;
-                auto run = [&](int u) {
+                u32x4(&t)[RUNS] = held[HOLD ? i * (FN / CF) + f0 / CF : 0];
+#pragma unroll
+                for (int u = 0; u < RUNS; ++u) {
                     const int row = u * STEP + row0;
-                    return *reinterpret_cast<const u32x4*>(area + row * ROW + (slot ^ (row & (SLOTS - 1))) * 16);
-                };
-                if (fast) {
-                    const uint32_t off = valid > 0 ? row0 * static_cast<uint32_t>(pitch) + c * ES : kOutOfRange;
-#pragma unroll
-                    for (int u = 0; u < SLOTS / 2; ++u)
-                        __builtin_amdgcn_raw_buffer_store_b128(
-                            run(u), y, off + (i * 32 + u * STEP) * static_cast<uint32_t>(pitch), 0, 0);
-                } else {
-#pragma nounroll
-                    for (int u = 0; u < SLOTS / 2; ++u) {
-                        const u32x4 t = run(u);
-                        const int row = i * 32 + u * STEP + row0;
-                        if (row >= rows || valid <= 0) continue;
-                        TY* dst = reinterpret_cast<TY*>(y0 + row * pitch) + c;
-                        if (valid >= RUN) {
-                            *reinterpret_cast<Raw16*>(dst) = Raw16{{t[0], t[1], t[2], t[3]}};
-                            continue;
-                        }
-#pragma unroll
-                        for (int j = 0; j < RUN; ++j)
-                            if (j < valid) {
-                                if constexpr (ES == 4)
-                                    dst[j] = __uint_as_float(t[j]);
-                                else
-                                    dst[j].bits = static_cast<uint16_t>(t[j / 2] >> (j % 2 * 16));
-                            }
-                    }
+                    t[u] = *reinterpret_cast<const u32x4*>(area + row * ROW + place(row, slot) * 16);
                 }
                 wave_sync();
+                if constexpr (!HOLD) store_turn(i, f0, t);
             }
+        before_stores();
+        if constexpr (HOLD)
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+#pragma unroll
+                for (int f0 = 0; f0 < FN; f0 += CF) store_turn(i, f0, held[i * (FN / CF) + f0 / CF]);
     } else {
+        before_stores();
         const __amdgpu_buffer_rsrc_t y = buffer(static_cast<uint8_t*>(p.y) + m0 * p.y_pitch, rows * p.y_pitch),
                                      ys = buffer(p.ys + m0 * p.y_spitch, rows * p.y_spitch);
 #pragma unroll
@@ -230,7 +268,7 @@ __device__ __forceinline__ void write_tile(const f32x16 (&acc)[FM][FN], Bias add
 }  // namespace mx
 
 // Few rows (k_mx_stream.hip).  `x`: MXFP4, or x's own type where mx_stream_takes_raw says so.
-bool mx_stream_supported(long long m);
+bool mx_stream_supported(long long m, int n, int k);
 bool mx_stream_takes_raw(long long m, int k);
 cfwd_status mx_stream(const mx::MatmulParams& p, cfwd_dtype x, cfwd_dtype y, hipStream_t st);
 
