@@ -385,7 +385,7 @@ size_t x_bytes(const cfwd_mx_matmul_desc* d) {  // of an x that the call quantis
 
 size_t mx_matmul_workspace(const cfwd_mx_matmul_desc* d) {
     const bool stream = mx_stream_supported(d->m, d->n, d->k);
-    const size_t x = d->x_dtype == CFWD_MXFP4 || (stream && mx_stream_takes_raw(d->m, d->k)) ? 0 : x_bytes(d);
+    const size_t x = d->x_dtype == CFWD_MXFP4 || (stream && mx_stream_takes_raw(d)) ? 0 : x_bytes(d);
     if (stream) return x;
     const Choice c = choose(d, compute_units());
     return x + (c.splits > 1 ? static_cast<size_t>(c.splits) * d->m * ((d->n + 3) / 4 * 4) * 4 : 0);
@@ -397,7 +397,7 @@ cfwd_status mx_matmul(const cfwd_mx_matmul_desc* d, const void* x, const void* x
     mx::MatmulParams p{};
     uint8_t* work = static_cast<uint8_t*>(workspace);
     const bool stream = mx_stream_supported(d->m, d->n, d->k);
-    const bool raw = d->x_dtype != CFWD_MXFP4 && stream && mx_stream_takes_raw(d->m, d->k);
+    const bool raw = d->x_dtype != CFWD_MXFP4 && stream && mx_stream_takes_raw(d);
     if (d->x_dtype != CFWD_MXFP4 && !raw) {
         uint8_t* scales = work + round256(static_cast<size_t>(d->m) * mx_code_pitch(d->k));
         const cfwd_status s = mx_quantize(d->m, d->k, d->x_dtype, x, d->x_stride, work, scales, st);

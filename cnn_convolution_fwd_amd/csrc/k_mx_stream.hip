@@ -9,9 +9,12 @@
 //
 // v_mfma_scale_f32_16x16x128_f8f6f4 with w as A and x as B: lane l holds block
 // l / 16 of the K step's four of row l % 16, of each operand, and ends with
-// columns 4 (l / 16) .. + 3 of y's row l % 16.  An x in 16 or 32 bits is
-// quantised on the way: a lane needs one whole block, so it reads the block's
-// 32 values and finds their scale without any exchange.
+// columns 4 (l / 16) .. + 3 of y's row l % 16.
+//
+// A small x in 16 or 32 bits is quantised on the way, by every workgroup for
+// itself, into LDS: its values are requested before the first weights, and
+// become codes while those are on their way (1 x 4096 -> 16384 in bf16: 14.5 us
+// with a quantisation by each lane of its own block at its use).
 #include "mx_matmul_impl.h"
 
 #include <type_traits>
@@ -20,31 +23,18 @@ namespace cfwd {
 namespace mx {
 
 constexpr int kWaves = 8;
-
-// An MXFP4 block's codes and scale byte from 32 values of x, the first at x[col].
-template <typename T>
-__device__ __forceinline__ i32x4 quantize32(const T* x, int valid, int* byte) {
-    float v[4][8];
-    uint32_t top = 0;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        load8(x + q * 8, valid - q * 8, v[q]);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) top = max(top, abs_bits(v[q][i]));
-    }
-    const uint32_t e = exponent_byte(top);
-    *byte = static_cast<int>(e);
-    return i32x4{static_cast<int>(encode8(v[0], e)), static_cast<int>(encode8(v[1], e)),
-                 static_cast<int>(encode8(v[2], e)), static_cast<int>(encode8(v[3], e))};
-}
+constexpr int kRawBlocks = 1024;  // of an x that the kernel quantises: 8 runs of 8 values a thread
 
 // MT: 16-row tiles of y.  TX: void for MXFP4, else x's type (p.x, p.x_stride
-// elements a row).  TY as in write_rows.
+// elements a row).  TY as in write_tile.
 template <int MT, int NF, typename TX, typename TY>
-__global__ __launch_bounds__(64 * kWaves) void stream_kernel(MatmulParams p) {
+__global__ __launch_bounds__(64 * kWaves) void stream_kernel(MatmulParams p, Divisor per_row) {
+    constexpr bool RAW = !std::is_void<TX>::value;
     constexpr int STEPS = 20 / (NF + MT);  // K steps in flight: what 100 registers of operands and scales hold
     constexpr int ROW = NF * 16 + 4;       // floats of a row of partial sums, padded against bank conflicts
     __shared__ __attribute__((aligned(16))) float part[kWaves][MT * 16 * ROW];
+    __shared__ __attribute__((aligned(16))) uint32_t xcodes[RAW ? kRawBlocks * 4 : 4];
+    __shared__ uint8_t xscales[RAW ? kRawBlocks : 4];
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n0 = xcd_linear(blockIdx.x, gridDim.x) * (16 * NF);
@@ -56,11 +46,11 @@ __global__ __launch_bounds__(64 * kWaves) void stream_kernel(MatmulParams p) {
                                  xs = buffer(p.xs, static_cast<long long>(m) * p.spitch);
     f32x4 acc[MT][NF] = {};
     const int steps = (p.kb + 3) / 4;
-    for (int s0 = wave; s0 < steps; s0 += kWaves * STEPS) {
-        i32x4 a[STEPS][NF], cx[STEPS][MT];
-        int sa[STEPS][NF], sx[STEPS][MT];
+    i32x4 a[STEPS][NF], cx[STEPS][MT];
+    int sa[STEPS][NF], sx[STEPS][MT];
+    auto request = [&](int s0) {  // steps past the end load nothing and multiply zeros
 #pragma unroll
-        for (int s = 0; s < STEPS; ++s) {  // steps past the end load nothing and multiply zeros
+        for (int s = 0; s < STEPS; ++s) {
             const int b = (s0 + s * kWaves) * 4 + g;
 #pragma unroll
             for (int f = 0; f < NF; ++f) {
@@ -69,7 +59,7 @@ __global__ __launch_bounds__(64 * kWaves) void stream_kernel(MatmulParams p) {
                                                         w, b < p.kb ? row * p.pitch + b * 16 : kOutOfRange, 0, 0));
                 sa[s][f] = __builtin_amdgcn_raw_buffer_load_b8(ws, b < p.kb ? row * p.spitch + b : kOutOfRange, 0, 0);
             }
-            if constexpr (std::is_void<TX>::value)
+            if constexpr (!RAW)
 #pragma unroll
                 for (int t = 0; t < MT; ++t) {
                     const int row = t * 16 + r;
@@ -79,6 +69,45 @@ __global__ __launch_bounds__(64 * kWaves) void stream_kernel(MatmulParams p) {
                 }
         }
         __builtin_amdgcn_sched_barrier(0);  // all of them are on their way before the first is waited for
+    };
+    if constexpr (RAW) {
+        // Runs of 8 values; one that crosses its row's end reads on into what follows, or zeros at x's end.
+        constexpr int RUNS = kRawBlocks * 4 / (64 * kWaves), WORDS = sizeof(TX) / 2;
+        const __amdgpu_buffer_rsrc_t gx = buffer(p.x, ((m - 1) * p.x_stride + p.k) * sizeof(TX));
+        u32x4 v[RUNS][WORDS];
+#pragma unroll
+        for (int i = 0; i < RUNS; ++i) {
+            const uint32_t u = threadIdx.x + i * 64 * kWaves, row = divide(u, per_row), q = u - row * per_row.d;
+            const uint32_t off = static_cast<int>(row) < m
+                                     ? static_cast<uint32_t>(row * p.x_stride + q * 8) * static_cast<uint32_t>(sizeof(TX))
+                                     : kOutOfRange;
+#pragma unroll
+            for (int j = 0; j < WORDS; ++j) v[i][j] = __builtin_amdgcn_raw_buffer_load_b128(gx, off + j * 16, 0, 0);
+        }
+        request(wave);
+#pragma unroll
+        for (int i = 0; i < RUNS; ++i) {
+            const uint32_t u = threadIdx.x + i * 64 * kWaves, row = divide(u, per_row), q = u - row * per_row.d;
+            float f[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                float e;
+                if constexpr (sizeof(TX) == 4) e = __uint_as_float(v[i][j / 4][j % 4]);
+                else e = __uint_as_float(j % 2 ? v[i][0][j / 2] & 0xffff0000u : v[i][0][j / 2] << 16);
+                f[j] = static_cast<int>(q * 8) + j < p.k ? e : 0.0f;
+            }
+            uint32_t byte;
+            const uint32_t codes = quantize8(f, &byte);
+            if (static_cast<int>(row) < m) {
+                xcodes[u] = codes;
+                if ((q & 3) == 0) xscales[u / 4] = static_cast<uint8_t>(byte);
+            }
+        }
+        __syncthreads();
+    } else {
+        request(wave);
+    }
+    for (int s0 = wave; s0 < steps;) {
 #pragma unroll
         for (int s = 0; s < STEPS; ++s) {
             const int b = (s0 + s * kWaves) * 4 + g;
@@ -86,11 +115,14 @@ __global__ __launch_bounds__(64 * kWaves) void stream_kernel(MatmulParams p) {
             for (int t = 0; t < MT; ++t) {
                 i32x4 c = {};
                 int sc = 0;
-                if constexpr (std::is_void<TX>::value) {
+                if constexpr (RAW) {
+                    if (r < m && b < p.kb) {
+                        c = *reinterpret_cast<const i32x4*>(&xcodes[(r * p.kb + b) * 4]);
+                        sc = xscales[r * p.kb + b];
+                    }
+                } else {
                     c = cx[s][t];
                     sc = sx[s][t];
-                } else if (r < m && b < p.kb) {
-                    c = quantize32(reinterpret_cast<const TX*>(p.x) + r * p.x_stride + b * 32, p.k - b * 32, &sc);
                 }
                 const i32x8 c8 = {c[0], c[1], c[2], c[3], 0, 0, 0, 0};
 #pragma unroll
@@ -101,6 +133,8 @@ __global__ __launch_bounds__(64 * kWaves) void stream_kernel(MatmulParams p) {
                 }
             }
         }
+        s0 += kWaves * STEPS;
+        if (s0 < steps) request(s0);
     }
 #pragma unroll
     for (int t = 0; t < MT; ++t)
@@ -136,11 +170,11 @@ template <int MT, int NF, typename TX>
 void launch_stream_y(const MatmulParams& p, cfwd_dtype y, hipStream_t st) {
     const unsigned grid = static_cast<unsigned>((p.n + 16 * NF - 1) / (16 * NF));
     if (y == CFWD_F32)
-        stream_kernel<MT, NF, TX, float><<<grid, 64 * kWaves, 0, st>>>(p);
+        stream_kernel<MT, NF, TX, float><<<grid, 64 * kWaves, 0, st>>>(p, divisor(p.kb * 4));
     else if (y == CFWD_BF16)
-        stream_kernel<MT, NF, TX, bf16_t><<<grid, 64 * kWaves, 0, st>>>(p);
+        stream_kernel<MT, NF, TX, bf16_t><<<grid, 64 * kWaves, 0, st>>>(p, divisor(p.kb * 4));
     else if constexpr (NF > 1)  // a block of 32 outputs is one workgroup's
-        stream_kernel<MT, NF, TX, void><<<grid, 64 * kWaves, 0, st>>>(p);
+        stream_kernel<MT, NF, TX, void><<<grid, 64 * kWaves, 0, st>>>(p, divisor(p.kb * 4));
 }
 
 template <int MT, typename TX>
@@ -156,9 +190,13 @@ void launch_stream_n(const MatmulParams& p, cfwd_dtype y, hipStream_t st) {
 
 }  // namespace mx
 
-// An x that is not MXFP4 is quantised by every workgroup; beyond these sizes
-// that costs more than one more launch.
-bool mx_stream_takes_raw(long long m, int k) { return m <= 16 && mx_blocks(k) <= 4 * 4 * mx::kWaves; }
+// One tile of rows, small enough for every workgroup to quantise it, with rows of whole words
+// (the last of a row is then in range as a whole) within a buffer's 31 bits.
+bool mx_stream_takes_raw(const cfwd_mx_matmul_desc* d) {
+    const long long es = d->x_dtype == CFWD_F32 ? 4 : 2;
+    return d->m <= 16 && d->m * mx_blocks(d->k) <= mx::kRawBlocks && d->k * es % 4 == 0 && d->x_stride * es % 4 == 0 &&
+           d->x_stride < (1 << 24);
+}
 
 // Beyond 32 rows every workgroup's reading of x counts: the tile kernel then
 // wins unless w is small (48 rows: 4096 x 4096 10.6 us here, 13.4 there; 11000 x

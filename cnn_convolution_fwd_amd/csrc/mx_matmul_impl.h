@@ -269,7 +269,7 @@ __device__ __forceinline__ void write_tile(const f32x16 (&acc)[FM][FN], Bias add
 
 // Few rows (k_mx_stream.hip).  `x`: MXFP4, or x's own type where mx_stream_takes_raw says so.
 bool mx_stream_supported(long long m, int n, int k);
-bool mx_stream_takes_raw(long long m, int k);
+bool mx_stream_takes_raw(const cfwd_mx_matmul_desc* d);
 cfwd_status mx_stream(const mx::MatmulParams& p, cfwd_dtype x, cfwd_dtype y, hipStream_t st);
 
 }  // namespace cfwd

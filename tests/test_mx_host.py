@@ -13,7 +13,7 @@ def status(st):
     return st, B.library().cfwd_last_error().decode()
 
 
-def matmul(m=4, n=8, k=64, x_dtype=B.BF16, y_dtype=B.F32, stride=64, act=0, x=P, xs=None, w=P * 2, ws=P * 3, bias=None,
+def matmul(m=70, n=8, k=64, x_dtype=B.BF16, y_dtype=B.F32, stride=64, act=0, x=P, xs=None, w=P * 2, ws=P * 3, bias=None,
            y=P * 4, ys=None, work=P * 5, work_bytes=1 << 20):
     d = B.MxMatmulDesc(m, n, k, x_dtype, y_dtype, stride, act)
     return status(B.library().cfwd_mx_matmul(ctypes.byref(d), x, xs, w, ws, bias, y, ys, work, work_bytes, None))
@@ -76,7 +76,7 @@ def test_matmul_workspace_and_size_limits():
         B.mx_matmul_workspace_size(d)
     assert e.value.status == B.ERR_UNSUPPORTED
     assert B.mx_matmul_workspace_size(B.MxMatmulDesc(0, 8, 64, B.BF16, B.F32, 64, 0)) == 0
-    assert B.mx_matmul_workspace_size(B.MxMatmulDesc(4, 8, 64, B.BF16, B.F32, 64, 0)) >= 4 * 32 + 4 * 4
+    assert B.mx_matmul_workspace_size(B.MxMatmulDesc(70, 8, 64, B.BF16, B.F32, 64, 0)) >= 70 * 32 + 70 * 4
 
 
 @pytest.mark.parametrize("kw", [dict(rows=-1), dict(c=0), dict(c=(1 << 22) + 1), dict(post=3), dict(pre=-1),
