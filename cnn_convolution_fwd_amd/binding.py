@@ -8,6 +8,7 @@ built, loading fails loudly -- there is no CPU fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import List, NamedTuple, Optional, Sequence, Tuple, Union
 
@@ -700,7 +701,7 @@ def _check_mx(t: MxTensor, what: str) -> int:
 def _guard(dev: int):
     """None when ``dev`` is the current GPU, else a context that makes it that (kernels go to the current GPU's stream)."""
     torch = _torch()
-    return None if dev == torch.cuda.current_device() else torch.cuda.device(dev)
+    return None if dev == torch._C._cuda_getDevice() else torch.cuda.device(dev)
 
 
 def _stream_of(dev: int) -> int:
@@ -769,6 +770,18 @@ def mx_dequantize(t: MxTensor, dtype="f32", out=None):
     return out
 
 
+@functools.lru_cache(maxsize=1024)
+def _mx_matmul_desc(*sizes):
+    """(descriptor reference, workspace bytes) of a product of these sizes; made once, read only."""
+    desc = MxMatmulDesc(*sizes)
+    return ctypes.byref(desc), mx_matmul_workspace_size(desc)
+
+
+@functools.lru_cache(maxsize=1024)
+def _gated_norm_desc(*sizes):
+    return ctypes.byref(GatedNormDesc(*sizes))
+
+
 def mx_matmul_workspace_size(desc: MxMatmulDesc) -> int:
     b = ctypes.c_size_t()
     _check(_lib().cfwd_mx_matmul_workspace_size(ctypes.byref(desc), ctypes.byref(b)))
@@ -829,16 +842,16 @@ def mx_matmul(x, w: MxTensor, bias=None, act: str = "none", out_dtype=None, out=
     if guard is not None:
         with guard:
             return mx_matmul(x, w, bias, act, None, out, workspace)
-    desc = MxMatmulDesc(rows, n, k, x_code, y_code, stride, act_code)
+    desc, ws_bytes = _mx_matmul_desc(rows, n, k, x_code, y_code, stride, act_code)
     if workspace is not None:
         ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    elif ws_bytes:
+        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=xt.device)
+        ws = workspace.data_ptr()
     else:
-        ws, ws_bytes = None, mx_matmul_workspace_size(desc)
-        if ws_bytes:
-            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=xt.device)
-            ws = workspace.data_ptr()
+        ws = None
     yp, ys = (out.codes.data_ptr(), out.scales.data_ptr()) if y_code == MXFP4 else (out.data_ptr(), None)
-    _check(_lib().cfwd_mx_matmul(ctypes.byref(desc), xt.data_ptr(), xs, w_codes.data_ptr(), w_scales.data_ptr(),
+    _check(_lib().cfwd_mx_matmul(desc, xt.data_ptr(), xs, w_codes.data_ptr(), w_scales.data_ptr(),
                                  _ptr(bias), yp, ys, ws, ws_bytes, _stream_of(dev)))
     return out
 
@@ -880,10 +893,9 @@ def gated_norm(b, residual=None, gate=None, residual_scale: float = 1.0, post: s
         if groups == 0 and rows:
             raise ValueError("gate has no rows")
         per = -(-rows // groups) if groups else 0
-    for name, t in (("post_weight", post_weight), ("post_bias", post_bias), ("pre_weight", pre_weight),
-                    ("pre_bias", pre_bias)):
+    for t in (post_weight, post_bias, pre_weight, pre_bias):
         if t is not None and (t.dtype != torch.float32 or t.shape != (c,)):
-            raise ValueError("%s must be float32 [%d]" % (name, c))
+            raise ValueError("weights and biases must be float32 [%d]" % c)
     post_code, pre_code = _code(_NORMS, post, "norm"), _code(_NORMS, pre, "norm")
     h_code = b_code if out_dtype is None else _code(_MX_CODES, out_dtype, "out_dtype")
     if out is not None:
@@ -908,16 +920,19 @@ def gated_norm(b, residual=None, gate=None, residual_scale: float = 1.0, post: s
     if pre_code == NORM_NONE:
         out, h_code = None, b_code
     elif out is None:
-        out = _new_mx(shape[:-1], c, like.device) if h_code == MXFP4 else \
-            torch.empty(shape, dtype=torch.float32 if h_code == F32 else torch.bfloat16, device=like.device)
+        if h_code == MXFP4:
+            out = _new_mx(shape[:-1], c, like.device)
+        else:
+            out = torch.empty_like(like) if b is not None else torch.empty(
+                shape, dtype=torch.float32 if h_code == F32 else torch.bfloat16, device=like.device)
     guard = _guard(dev)
     if guard is not None:
         with guard:
             return gated_norm(b, residual, gate, residual_scale, post, post_weight, post_bias, pre, pre_weight,
                               pre_bias, eps, out_dtype, sum_out, out, want_sum)
-    desc = GatedNormDesc(rows, c, per, residual_scale, eps, post_code, pre_code, b_code, s_code, h_code)
+    desc = _gated_norm_desc(rows, c, per, residual_scale, eps, post_code, pre_code, b_code, s_code, h_code)
     hp, hs = (out.codes.data_ptr(), out.scales.data_ptr()) if h_code == MXFP4 else (_ptr(out), None)
-    _check(_lib().cfwd_gated_norm(ctypes.byref(desc), _ptr(b), _ptr(residual), _ptr(gate), _ptr(post_weight),
+    _check(_lib().cfwd_gated_norm(desc, _ptr(b), _ptr(residual), _ptr(gate), _ptr(post_weight),
                                   _ptr(post_bias), _ptr(pre_weight), _ptr(pre_bias), _ptr(sum_out), hp, hs,
                                   _stream_of(dev)))
     return sum_out, out

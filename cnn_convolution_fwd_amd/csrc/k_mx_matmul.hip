@@ -31,13 +31,30 @@ __device__ __forceinline__ void wait_loads() {  // until at most N of this wave'
 // All waves of the workgroup; what memory accesses the code has before and after stays there.
 __device__ __forceinline__ void barrier() { asm volatile("s_barrier" ::: "memory"); }
 
-// Tiles through LDS.  A tile is 64 F rows of y x 64 F columns; the four waves
-// (2 x 2) of a workgroup take 32 F x 32 F of it each.  With F = 2 the grid is
-// what fits the device at once, and each workgroup works through several tiles
-// as one unbroken run of stages of 128 values of K, so that a tile's output
-// pass finds the next tile's operands on their way.  With F = 4, for long sums,
-// a workgroup has one tile: its 256 accumulators leave no registers in which
-// the next operands could outlast the output pass.
+struct Tiling {
+    int tiles_m, tiles_n;
+    int splits, split_stages;  // parts of the sum over K, each with its own y (m x ldy) behind the last; stages of a part
+    Divisor tiles;             // of one part
+    Divisor group, height, last_height;  // of tiles in a group of 8 rows of tiles; of rows in a group, in the last one
+};
+
+// The u-th tile, of BxB: the order goes down columns of 8 tiles, part by part.
+template <int B>
+__device__ __forceinline__ void tile_place(const Tiling& order, int u, long long* m0, int* n0, int* split) {
+    *split = divide(u, order.tiles);
+    const int t = u - *split * order.tiles.d;
+    const int group = divide(t, order.group), in_group = t - group * order.group.d;
+    const Divisor height = group == (order.tiles_m - 1) / 8 ? order.last_height : order.height;
+    const int column = divide(in_group, height);
+    *m0 = static_cast<long long>(group * 8 + in_group - column * height.d) * B;
+    *n0 = column * B;
+}
+
+// Tiles through LDS: 128 rows of y x 128 columns; the four waves (2 x 2) of a
+// workgroup take 64 x 64 each.  The grid is what fits the device at once, two
+// workgroups on a CU, and each works through several tiles as one unbroken run of
+// stages of 128 values of K, so that a tile's output pass finds the next tile's
+// operands on their way.
 //
 // LDS holds four stages in turn.  While stage s is multiplied, s + 1 is whole,
 // s + 2 is on its way and s + 3 is requested, so the operands of the next
@@ -48,7 +65,7 @@ __device__ __forceinline__ void barrier() { asm volatile("s_barrier" ::: "memory
 //
 // Scales come four stages ("a group") at a time, so that a 16-byte run of each
 // row is read at once: a word at a time costs a cache line for every word
-// (8192^3: 368 us so, 306 us without any scale copies).
+// (8192^3: 524 us so, 405 in groups).
 //
 // A stage's row is 64 bytes, four blocks, of which half h of a wave takes
 // blocks 2 h and 2 h + 1.  LDS serves 16 lanes' 16 bytes at once if they cover
@@ -58,17 +75,10 @@ __device__ __forceinline__ void barrier() { asm volatile("s_barrier" ::: "memory
 //
 // The output pass of the tile uses the LDS of the stage multiplied last, which
 // is filled again only after the next stage's barrier.
-struct Tiling {
-    int tiles_m, tiles_n;
-    int splits, split_stages;  // parts of the sum over K, each with its own y (m x ldy) behind the last; stages of a part
-    Divisor tiles;             // of one part
-    Divisor group, height, last_height;  // of tiles in a group of 8 rows of tiles; of rows in a group, in the last one
-};
 
-template <int F, typename TY>
-__global__ __launch_bounds__(256, F > 2 ? 1 : 2) void tile_kernel(MatmulParams p, Tiling order, bool fast) {
-    static_assert(F == 2 || F == 4, "the copies below are laid out for these");
-    constexpr int B = 64 * F, STAGE = 2 * B * 64, GROUP = 2 * B * 16;
+template <typename TY>
+__global__ __launch_bounds__(256, 2) void tile_kernel(MatmulParams p, Tiling order, bool fast) {
+    constexpr int F = 2, B = 64 * F, STAGE = 2 * B * 64, GROUP = 2 * B * 16;
     constexpr int CODE_LOADS = 2 * F, SCALE_LOADS = 2 * F;  // a wave's copies for a stage, for a group
     constexpr int STORES = stores<F, F, TY>();
     __shared__ __attribute__((aligned(128))) uint8_t lds[4 * STAGE + 4 * GROUP];
@@ -76,20 +86,12 @@ __global__ __launch_bounds__(256, F > 2 ? 1 : 2) void tile_kernel(MatmulParams p
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave >> 1, wn = wave & 1;
 
-    // The i-th tile of this workgroup.  A round of tiles is a run of the tiles'
-    // order, each XCD a run within it; the order goes down columns of 8 tiles.
+    // The i-th tile of this workgroup.  A round of tiles is a run of their order, each XCD a run within it.
     const int tiles = order.tiles.d * order.splits;
-    const int rounds = F > 2 ? 1 : (tiles - 1 - static_cast<int>(blockIdx.x)) / static_cast<int>(gridDim.x) + 1;
+    const int rounds = (tiles - 1 - static_cast<int>(blockIdx.x)) / static_cast<int>(gridDim.x) + 1;
     auto tile_at = [&](int i, long long* m0, int* n0, int* split) {
         const int first = i * gridDim.x;
-        const int u = first + xcd_linear(blockIdx.x, min(static_cast<int>(gridDim.x), tiles - first));
-        *split = divide(u, order.tiles);
-        const int t = u - *split * order.tiles.d;
-        const int group = divide(t, order.group), in_group = t - group * order.group.d;
-        const Divisor height = group == (order.tiles_m - 1) / 8 ? order.last_height : order.height;
-        const int column = divide(in_group, height);
-        *m0 = static_cast<long long>(group * 8 + in_group - column * height.d) * B;
-        *n0 = column * B;
+        tile_place<B>(order, first + xcd_linear(blockIdx.x, min(static_cast<int>(gridDim.x), tiles - first)), m0, n0, split);
     };
 
     const int all_stages = (p.kb + 3) / 4;
@@ -189,12 +191,11 @@ __global__ __launch_bounds__(256, F > 2 ? 1 : 2) void tile_kernel(MatmulParams p
         const int stages = stages_of(split);
         m0 += wm * 32 * F;
         n0 += wn * 32 * F;
-        float bias[F > 2 ? 1 : F][16];
-        if constexpr (F == 2)  // requested ahead of the output pass; wider tiles have no registers for that
-            if (p.bias) {
+        float bias[F][16];
+        if (p.bias) {  // requested ahead of the output pass
 #pragma unroll
-                for (int f = 0; f < F; ++f) load_bias(p, n0 + f * 32, bias[f]);
-            }
+            for (int f = 0; f < F; ++f) load_bias(p, n0 + f * 32, bias[f]);
+        }
         for (int stage = 0; stage < stages; ++stage, ++count, ++since) {
             // This wave's copies for the next stage: those for the one after it, and stores, may be outstanding.
             if (since < 2) {
@@ -240,14 +241,12 @@ __global__ __launch_bounds__(256, F > 2 ? 1 : 2) void tile_kernel(MatmulParams p
         barrier();  // the last stage's LDS is no longer read
         auto add_bias = [&](int f, float(&v)[16]) {
             if (!p.bias) return;
-            if constexpr (F > 2) load_bias(p, n0 + f * 32, bias[0]);
 #pragma unroll
-            for (int j = 0; j < 16; ++j) v[j] += bias[F > 2 ? 0 : f][j];
+            for (int j = 0; j < 16; ++j) v[j] += bias[f][j];
         };
         MatmulParams part = p;
         if constexpr (std::is_same<TY, float>::value) part.y = static_cast<float*>(p.y) + split * p.m * p.ldy;
-        write_tile<F, F, TY, false>(acc, add_bias, part, m0, n0, fast,
-                                    lds + ((count - 1) & 3) * STAGE + wave * (STAGE / 4), [] {});
+        write_tile<F, F, TY>(acc, add_bias, part, m0, n0, fast, lds + ((count - 1) & 3) * STAGE + wave * (STAGE / 4));
         if (!fast) wait_loads<0>();  // an unknown number of stores
 #pragma unroll
         for (int i = 0; i < F; ++i)
@@ -256,6 +255,147 @@ __global__ __launch_bounds__(256, F > 2 ? 1 : 2) void tile_kernel(MatmulParams p
         since = 0;
     }
     wait_loads<0>();  // no copy may reach LDS after the workgroup has ended
+}
+
+// Wide tiles, for long sums over many tiles: 256 rows of y x 256 columns, one
+// tile a workgroup, one workgroup a CU, 128 x 128 a wave: half the copies of the
+// kernel above for the same products.  (256 accumulators a lane leave no
+// registers in which the next tile's operands could outlast the output pass.)
+//
+// A stage is 256 values of K here, its rows 128 bytes: a copy costs by the cache
+// line that it touches, whatever it takes of it (from L2 134 GB/s a CU in whole
+// lines, 69 GB/s in halves).  LDS holds two stages.  A stage's matrix
+// instructions are four steps, whose operands are read one step ahead; before
+// the last of them all of the stage is in registers, and there the waves meet:
+// the next stage is whole, and the copies of the one after it begin, over the one
+// just read, spread over the matrix instructions of this step and the next
+// (8192^3: 281 us with all of them in one step, 269 so, 231 without copies; 305
+// with four stages of 128 values).
+//
+// Block b of row i lies in slot b ^ ((i >> 1) & 7), scale word q of a row's 8 (four
+// stages', "a chunk") at q ^ (2 ((i >> 3) & 3)): 16 rows' reads of one block
+// then cover the 64 banks (with i & 7, conflicts took 62% of LDS's cycles).
+template <typename TY>
+__global__ __launch_bounds__(256, 1) void wide_kernel(MatmulParams p, Tiling order, bool fast) {
+    constexpr int F = 4, B = 64 * F, STAGE = 2 * B * 128, CHUNK = 2 * B * 32;
+    __shared__ __attribute__((aligned(128))) uint8_t lds[2 * STAGE + 2 * CHUNK];
+    const int lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave >> 1, wn = wave & 1;
+    long long m0;
+    int n0, split;
+    tile_place<B>(order, xcd_linear(blockIdx.x, gridDim.x), &m0, &n0, &split);
+    const int stages = (p.kb + 7) / 8;
+    const long long rows_x = min(static_cast<long long>(B), p.m - m0), rows_w = min(B, p.n - n0);
+    const __amdgpu_buffer_rsrc_t gx = buffer(p.x + m0 * p.pitch, rows_x * p.pitch),
+                                 gxs = buffer(p.xs + m0 * p.spitch, rows_x * p.spitch),
+                                 gw = buffer(p.w + static_cast<long long>(n0) * p.pitch, rows_w * p.pitch),
+                                 gws = buffer(p.ws + static_cast<long long>(n0) * p.spitch, rows_w * p.spitch);
+    const uint32_t lds0 = static_cast<uint32_t>(
+        reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t*)lds));
+
+    // one copy: 8 rows' codes of a stage, or 8 rows' scales of a chunk
+    const int copy_row = wave * 8 + (lane >> 3);
+    const int copy_block = (lane & 7) ^ ((copy_row >> 1) & 7), copy_word = (lane & 7) ^ (2 * (wave & 3));
+    const uint32_t copy_off = copy_row * p.pitch + copy_block * 16, copy_soff = copy_row * p.spitch + copy_word * 4;
+    auto copy_codes = [&](int stage, int i) {  // i-th of each operand's 8 copies
+        const uint32_t off = stage * 8 + copy_block < p.kb ? copy_off + stage * 128 : kOutOfRange;
+        const uint32_t to = lds0 + (stage & 1) * STAGE + wave * 1024 + i * 4096;
+        load_to_lds16(gw, off + i * 32 * p.pitch, to);
+        load_to_lds16(gx, off + i * 32 * p.pitch, to + B * 128);
+    };
+    auto copy_scales = [&](int part, int i) {  // i-th of 4 copies: quarter part % 4 of chunk part / 4, half the rows of w or of x
+        const int chunk = part >> 2, half = (part & 1) * (B / 2);
+        const uint32_t off = chunk * 32 + copy_word * 4 < p.spitch ? copy_soff + chunk * 32 : kOutOfRange;
+        const uint32_t to = lds0 + 2 * STAGE + (chunk & 1) * CHUNK + (part & 2) / 2 * (B * 32) + half * 32 + wave * 256 + i * 1024;
+        load_to_lds4(part & 2 ? gxs : gws, off + (half + i * 32) * p.spitch, to);
+    };
+
+    i32x4 a[2][F], b[2][F];  // operands of two steps in turn
+    int sw[2][F], sx[2][F];  // scale words of a stage, and of the next
+    const uint8_t* lw = lds + (wn * 32 * F + r) * 128;
+    const uint8_t* lx = lds + (B + wm * 32 * F + r) * 128;
+    const uint8_t* lws = lds + 2 * STAGE + (wn * 32 * F + r) * 32;
+    const uint8_t* lxs = lds + 2 * STAGE + (B + wm * 32 * F + r) * 32;
+    auto read_pair = [&](int stage, int j, int f) {
+        const int at = (stage & 1) * STAGE + ((4 * h + j) ^ ((r >> 1) & 7)) * 16 + f * 4096;
+        a[j & 1][f] = *reinterpret_cast<const i32x4*>(lw + at);
+        b[j & 1][f] = *reinterpret_cast<const i32x4*>(lx + at);
+    };
+    auto read_scales = [&](int stage, int set, int f) {
+        const int at = (stage >> 2 & 1) * CHUNK + (((stage & 3) * 2 + h) ^ (2 * (r >> 3))) * 4 + f * 1024;
+        sw[set][f] = *reinterpret_cast<const int*>(lws + at);
+        sx[set][f] = *reinterpret_cast<const int*>(lxs + at);
+    };
+    f32x16 acc[F][F] = {};
+    auto multiply = [&](auto j, int i) {
+        constexpr int J = decltype(j)::value;
+#pragma unroll
+        for (int f = 0; f < F; ++f) acc[i][f] = mfma<J>(a[J & 1][f], b[J & 1][i], acc[i][f], sw[0][f], sx[0][i]);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+
+#pragma unroll
+    for (int i = 0; i < 8; ++i) copy_codes(0, i);
+#pragma unroll
+    for (int q = 0; q < 5; ++q)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) copy_scales(q, i);
+    wait_loads<0>();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) copy_codes(1, i);
+    barrier();
+#pragma unroll
+    for (int f = 0; f < F; ++f) {
+        read_scales(0, 0, f);
+        read_pair(0, 0, f);
+    }
+    for (int s = 0; s < stages; ++s) {
+#pragma unroll
+        for (int i = 0; i < F; ++i) {
+            copy_codes(s + 1, 4 + i);
+            read_pair(s, 1, i);
+            multiply(std::integral_constant<int, 0>{}, i);
+        }
+#pragma unroll
+        for (int i = 0; i < F; ++i) {
+            read_pair(s, 2, i);
+            multiply(std::integral_constant<int, 1>{}, i);
+        }
+#pragma unroll
+        for (int i = 0; i < F; ++i) {
+            read_pair(s, 3, i);
+            multiply(std::integral_constant<int, 2>{}, i);
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // all of this stage is in registers
+        wait_loads<0>();
+        barrier();
+#pragma unroll
+        for (int i = 0; i < F; ++i) {
+            copy_codes(s + 2, i);
+            copy_scales(s + 5, i);  // a chunk's last quarter two stages before its first stage
+            read_pair(s + 1, 0, i);
+            read_scales(s + 1, 1, i);
+            multiply(std::integral_constant<int, 3>{}, i);
+        }
+#pragma unroll
+        for (int f = 0; f < F; ++f) {
+            sw[0][f] = sw[1][f];
+            sx[0][f] = sx[1][f];
+        }
+    }
+    wait_loads<0>();  // the copies past the last stage, which wrote zeros
+    barrier();
+    m0 += wm * 32 * F;
+    n0 += wn * 32 * F;
+    auto add_bias = [&](int f, float(&v)[16]) {
+        if (!p.bias) return;
+        float q[16];
+        load_bias(p, n0 + f * 32, q);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[j] += q[j];
+    };
+    write_tile<F, F, TY>(acc, add_bias, p, m0, n0, fast, lds + wave * (STAGE / 4));
 }
 
 // The parts of a split sum, one behind the other -> y.  A thread owns 8 columns.
@@ -284,24 +424,23 @@ __global__ __launch_bounds__(256) void join_kernel(MatmulParams p, const float* 
     store_run<TY>(p, row, n, valid, v);
 }
 
-template <int F>
-void launch_tiles(const MatmulParams& p, cfwd_dtype y, int splits, int cus, hipStream_t st) {
-    const int tiles_m = static_cast<int>((p.m + 64 * F - 1) / (64 * F)), tiles_n = (p.n + 64 * F - 1) / (64 * F);
+template <typename TY>
+void launch_tiles(const MatmulParams& p, bool wide, int splits, int cus, hipStream_t st) {
+    const int side = wide ? 256 : 128;
+    const int tiles_m = static_cast<int>((p.m + side - 1) / side), tiles_n = (p.n + side - 1) / side;
     const int stages = (p.kb + 3) / 4, split_stages = splits > 1 ? (stages + 4 * splits - 1) / (4 * splits) * 4 : stages;
     const int parts = (stages + split_stages - 1) / split_stages;
     const Tiling order{tiles_m, tiles_n, parts, split_stages, divisor(tiles_m * tiles_n), divisor(8u * tiles_n),
                        divisor(8), divisor((tiles_m - 1) % 8 + 1)};
-    const int tiles = tiles_m * tiles_n * parts, slots = 2 * cus;
-    const unsigned grid = static_cast<unsigned>(F > 2 || tiles < slots ? tiles : slots);
+    const int tiles = tiles_m * tiles_n * parts;
     // whole 16-byte runs, and a wave's rows within a buffer's 31 bits
-    const int es = y == CFWD_F32 ? 4 : 2;
-    const bool fast = y == CFWD_MXFP4 || (p.ldy * es % 16 == 0 && reinterpret_cast<uintptr_t>(p.y) % 16 == 0 && p.n <= (1 << 21));
-    if (y == CFWD_F32)
-        tile_kernel<F, float><<<grid, 256, 0, st>>>(p, order, fast);
-    else if (y == CFWD_BF16)
-        tile_kernel<F, bf16_t><<<grid, 256, 0, st>>>(p, order, fast);
+    constexpr int ES = std::is_same<TY, float>::value ? 4 : 2;
+    const bool fast = std::is_void<TY>::value ||
+                      (p.ldy * ES % 16 == 0 && reinterpret_cast<uintptr_t>(p.y) % 16 == 0 && p.n <= (1 << 21));
+    if (wide)
+        wide_kernel<TY><<<static_cast<unsigned>(tiles), 256, 0, st>>>(p, order, fast);
     else
-        tile_kernel<F, void><<<grid, 256, 0, st>>>(p, order, fast);
+        tile_kernel<TY><<<static_cast<unsigned>(tiles < 2 * cus ? tiles : 2 * cus), 256, 0, st>>>(p, order, fast);
 }
 
 // A split sum: parts in fp32 to `work`, then the joining pass.
@@ -313,7 +452,7 @@ void launch_split(const MatmulParams& p, cfwd_dtype y, int splits, int cus, floa
     q.act = CFWD_ACT_NONE;
     q.y = work;
     q.ldy = (p.n + 3) / 4 * 4;
-    launch_tiles<2>(q, CFWD_F32, splits, cus, st);
+    launch_tiles<float>(q, false, splits, cus, st);
     q = p;
     q.ldy = (p.n + 3) / 4 * 4;
     const Divisor per_row = divisor(y == CFWD_MXFP4 ? p.y_pitch / 4 : (p.n + 7) / 8);
@@ -342,36 +481,37 @@ int compute_units() {  // of the current device; asked for once
     return n;
 }
 
-// How a product of more rows than the stream kernel takes is cut up: F of the
-// tile kernel, and parts of the sum over K.
+// How a product of more rows than the stream kernel takes is cut up: wide
+// tiles or not, and parts of the sum over K.
 struct Choice {
-    int f, splits;
+    bool wide;
+    int splits;
 };
 
 // The cheapest by a model of the time, in us, fitted to measurements over sums
-// of 4 to 128 stages and 8 to 6000 tiles (n, m = 128 .. 100352), which it meets
-// to about 20%: a round of tiles takes its stages and an output pass; 128-wide
-// tiles share a CU by twos, or run twice as fast alone (8192 x 8192 x 8192: 405
-// us with F = 2, 305 with F = 4; x 1024: 75 and 76; 25088 x 512 x 256: 13 and
-// 16).  A split sum pays for its parts' traffic and a second launch (128 x 1024
+// of 2 to 128 stages and 8 to 6000 tiles: a round of tiles takes its stages and
+// an output pass; 128-wide tiles share a CU by twos, or run more than twice as
+// fast alone (narrow and wide: 8192 x 8192 x 8192 420 and 269 us; x 1024: 76 and
+// 73; x 512: 52 and 59; 25088 x 512 x 256: 13 and 16; 100352 x 1024 x 256: 55 and
+// 85).  A split sum pays for its parts' traffic and a second launch (128 x 1024
 // x 16384: 48 us whole, 19 in 8 parts; 500 x 4096 x 4096: 17 and 26 in 2).
 Choice choose(const cfwd_mx_matmul_desc* d, int cus) {
     const double stages = static_cast<double>((mx_blocks(d->k) + 3) / 4);
     const long long t2 = (d->m + 127) / 128 * ((d->n + 127) / 128), t4 = (d->m + 255) / 256 * ((d->n + 255) / 256);
     auto rounds = [](long long tiles, long long slots) { return static_cast<double>((tiles + slots - 1) / slots); };
-    const double alone = 0.36, shared = 0.74, wide = 1.05;  // us a stage
+    const double alone = 0.36, shared = 0.9, wide = 0.82;  // us for 128 values of K
     double best = t2 <= cus ? stages * alone + 2 : rounds(t2, 2 * cus) * (stages * shared + 3.4);
-    Choice c{2, 1};
-    const double four = rounds(t4, cus) * (stages * wide + 10);
+    Choice c{false, 1};
+    const double four = rounds(t4, cus) * (stages * wide + 11.5);
     if (four < best) {
         best = four;
-        c = {4, 1};
+        c = {true, 1};
     }
     for (int s = 2; s <= 8 && t2 * s <= cus && stages >= 4 * s; s *= 2) {
         const double split = stages / s * alone + 2 + 4 + static_cast<double>(d->m) * d->n * 8 * s / 4e6;
         if (split < best) {
             best = split;
-            c = {2, s};
+            c = {false, s};
         }
     }
     return c;
@@ -429,10 +569,12 @@ cfwd_status mx_matmul(const cfwd_mx_matmul_desc* d, const void* x, const void* x
     const Choice c = choose(d, cus);
     if (c.splits > 1)
         mx::launch_split(p, d->y_dtype, c.splits, cus, reinterpret_cast<float*>(work), st);
-    else if (c.f == 4)
-        mx::launch_tiles<4>(p, d->y_dtype, 1, cus, st);
+    else if (d->y_dtype == CFWD_F32)
+        mx::launch_tiles<float>(p, c.wide, 1, cus, st);
+    else if (d->y_dtype == CFWD_BF16)
+        mx::launch_tiles<bf16_t>(p, c.wide, 1, cus, st);
     else
-        mx::launch_tiles<2>(p, d->y_dtype, 1, cus, st);
+        mx::launch_tiles<void>(p, c.wide, 1, cus, st);
     return check_hip(hipGetLastError(), "MXFP4 product launch");
 }
 

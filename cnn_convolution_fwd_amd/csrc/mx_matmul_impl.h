@@ -78,13 +78,11 @@ __device__ __forceinline__ void store_run(const MatmulParams& p, long long row, 
 // on, with bias (add_bias(f, v) adds that of columns' fragment f), activation
 // and the one rounding.
 //
-// fp32 and bf16 results take a turn through the wave's own LDS area (32 rows x
-// TURN bytes, 16-byte slots permuted by row instead of padded), so that whole
-// runs of columns are stored.  HOLD: all runs are held in registers,
-// before_stores() is called when the wave is done with LDS, and then they are
-// stored; otherwise each turn's as it comes.  An MXFP4 block (32 columns of a
-// row) is spread over the two lanes r and r + 32, which exchange halves of two
-// blocks, so that each then holds a block's 16 bytes.
+// fp32 and bf16 results take a turn through the wave's own LDS area (32 rows, of
+// one or half a set of columns' fragments; 16-byte slots permuted by row instead
+// of padded), so that whole runs of columns are stored.  An MXFP4 block (32
+// columns of a row) is spread over the two lanes r and r + 32, which exchange
+// halves of two blocks, so that each then holds a block's 16 bytes.
 //
 // `fast`: rows of y are whole 16-byte runs, which leave as buffer stores,
 // out-of-range ones dropped by the hardware: each wave then issues exactly
@@ -126,9 +124,9 @@ __device__ __forceinline__ void load_bias(const MatmulParams& p, int n, float (&
     }
 }
 
-template <int FM, int FN, typename TY, bool HOLD, typename Bias, typename Before>
+template <int FM, int FN, typename TY, typename Bias>
 __device__ __forceinline__ void write_tile(const f32x16 (&acc)[FM][FN], Bias add_bias, const MatmulParams& p,
-                                           long long m0, int n0, bool fast, uint8_t* area, Before before_stores) {
+                                           long long m0, int n0, bool fast, uint8_t* area) {
     int lane = threadIdx.x & 63;
     asm volatile("" : "+v"(lane));  // keeps the pass's many addresses from being computed, and held, outside the caller's loop
     const int r = lane & 31, h = lane >> 5;
@@ -136,13 +134,12 @@ __device__ __forceinline__ void write_tile(const f32x16 (&acc)[FM][FN], Bias add
     if constexpr (!std::is_void<TY>::value) {
         constexpr int ES = sizeof(TY), CF = ES == 4 ? FN / 2 : FN;  // columns' fragments of one turn
         constexpr int ROW = CF * 32 * ES, SLOTS = ROW / 16, RUN = 16 / ES;
-        constexpr int TURNS = FM * FN / CF, RUNS = SLOTS / 2, STEP = 64 / SLOTS;  // runs of a lane; rows of one access of the wave
+        constexpr int RUNS = SLOTS / 2, STEP = 64 / SLOTS;  // of a lane in a turn; rows of one access of the wave
         const long long pitch = static_cast<long long>(p.ldy) * ES;
         uint8_t* y0 = static_cast<uint8_t*>(p.y) + m0 * pitch + static_cast<long long>(n0) * ES;
         const __amdgpu_buffer_rsrc_t y = buffer(y0, (rows - 1) * pitch + (static_cast<long long>(p.ldy) - n0) * ES);
         const int row0 = lane / SLOTS, slot = lane % SLOTS;
         auto place = [](int row, int at) { return at ^ ((SLOTS > 8 ? row : row >> 1) & (SLOTS - 1)); };
-        u32x4 held[HOLD ? TURNS : 1][RUNS];
         auto store_turn = [&](int i, int f0, const u32x4(&t)[RUNS]) {
             const int c = f0 * 32 + slot * RUN, valid = p.n - n0 - c;
             if (fast) {
@@ -194,23 +191,16 @@ __device__ __forceinline__ void write_tile(const f32x16 (&acc)[FM][FN], Bias add
                     }
                 }
                 wave_sync();
-                u32x4(&t)[RUNS] = held[HOLD ? i * (FN / CF) + f0 / CF : 0];
+                u32x4 t[RUNS];
 #pragma unroll
                 for (int u = 0; u < RUNS; ++u) {
                     const int row = u * STEP + row0;
                     t[u] = *reinterpret_cast<const u32x4*>(area + row * ROW + place(row, slot) * 16);
                 }
                 wave_sync();
-                if constexpr (!HOLD) store_turn(i, f0, t);
+                store_turn(i, f0, t);
             }
-        before_stores();
-        if constexpr (HOLD)
-#pragma unroll
-            for (int i = 0; i < FM; ++i)
-#pragma unroll
-                for (int f0 = 0; f0 < FN; f0 += CF) store_turn(i, f0, held[i * (FN / CF) + f0 / CF]);
     } else {
-        before_stores();
         const __amdgpu_buffer_rsrc_t y = buffer(static_cast<uint8_t*>(p.y) + m0 * p.y_pitch, rows * p.y_pitch),
                                      ys = buffer(p.ys + m0 * p.y_spitch, rows * p.y_spitch);
 #pragma unroll
