@@ -398,6 +398,159 @@ __global__ __launch_bounds__(256, 1) void wide_kernel(MatmulParams p, Tiling ord
     write_tile<F, F, TY>(acc, add_bias, p, m0, n0, fast, lds + wave * (STAGE / 4));
 }
 
+// Few tiles, no more than CUs: 128 x 128 of y, or of one part of a split sum, a
+// workgroup, alone on its CU.  Two groups of four waves share each stage's
+// products: group g takes steps 2 g and 2 g + 1, so every SIMD has two waves to
+// alternate between, and the groups' sums meet in LDS at the end, each group
+// finishing half of each wave's rows (500 x 4096 x 4096: 13.7 us, 17.6 with the
+// narrow kernel; 2048 x 2048 x 8192: 26 and 34).
+//
+// A stage is 256 values of K (whole cache lines, rows and slots as in the wide
+// kernel); LDS holds four, used as by the narrow kernel: s is multiplied, s + 1
+// is whole, s + 2 on its way, s + 3 requested.  Scales come in chunks of four
+// stages, a quarter with each stage's copies, into three areas in turn.
+template <typename TY>
+__global__ __launch_bounds__(512, 1) void pair_kernel(MatmulParams p, Tiling order, bool fast) {
+    constexpr int F = 2, B = 64 * F, STAGE = 2 * B * 128, CHUNK = 2 * B * 32;
+    constexpr int LOADS = 5;  // a wave's copies in one stage
+    __shared__ __attribute__((aligned(128))) uint8_t lds[4 * STAGE + 3 * CHUNK];
+    const int lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int half = wave >> 2, wm = wave >> 1 & 1, wn = wave & 1;
+    long long m0;
+    int n0, split;
+    tile_place<B>(order, xcd_linear(blockIdx.x, gridDim.x), &m0, &n0, &split);
+    const int first = split * order.split_stages / 2, stages = min(order.split_stages / 2, (p.kb + 7) / 8 - first);
+    const long long rows_x = min(static_cast<long long>(B), p.m - m0), rows_w = min(B, p.n - n0);
+    const __amdgpu_buffer_rsrc_t gx = buffer(p.x + m0 * p.pitch, rows_x * p.pitch),
+                                 gxs = buffer(p.xs + m0 * p.spitch, rows_x * p.spitch),
+                                 gw = buffer(p.w + static_cast<long long>(n0) * p.pitch, rows_w * p.pitch),
+                                 gws = buffer(p.ws + static_cast<long long>(n0) * p.spitch, rows_w * p.spitch);
+    const uint32_t lds0 = static_cast<uint32_t>(
+        reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t*)lds));
+
+    // one copy: 8 rows' codes of a stage, or 8 rows' scales of a chunk
+    const int copy_row = wave * 8 + (lane >> 3);
+    const int copy_block = (lane & 7) ^ ((copy_row >> 1) & 7), copy_word = (lane & 7) ^ (2 * (wave & 3));
+    const uint32_t copy_off = copy_row * p.pitch + copy_block * 16, copy_soff = copy_row * p.spitch + copy_word * 4;
+    auto copy_stage = [&](int s, int i) {  // i-th of each operand's 2 copies of stage s
+        const int stage = first + s;
+        const uint32_t off = s < stages && stage * 8 + copy_block < p.kb ? copy_off + stage * 128 : kOutOfRange;
+        const uint32_t to = lds0 + (s & 3) * STAGE + wave * 1024 + i * 8192;
+        load_to_lds16(gw, off + i * 64 * p.pitch, to);
+        load_to_lds16(gx, off + i * 64 * p.pitch, to + B * 128);
+    };
+    auto copy_scales = [&](int part) {  // quarter part % 4 of chunk part / 4: half the rows of w, or of x
+        const int chunk = part >> 2, rows = (part & 1) * (B / 2);
+        const uint32_t off = (first * 2 + chunk * 8 + copy_word) * 4 < p.spitch ? copy_soff + (first * 2 + chunk * 8) * 4 : kOutOfRange;
+        const uint32_t to = lds0 + 4 * STAGE + chunk % 3 * CHUNK + (part & 2) / 2 * (B * 32) + rows * 32 + wave * 256;
+        load_to_lds4(part & 2 ? gxs : gws, off + rows * p.spitch, to);
+    };
+
+    i32x4 a[2][F], b[2][F];  // operands of two steps in turn
+    int sw[2][F], sx[2][F];  // scale words of a stage, and of the next
+    const uint8_t* lw = lds + (wn * 32 * F + r) * 128;
+    const uint8_t* lx = lds + (B + wm * 32 * F + r) * 128;
+    const uint8_t* lws = lds + 4 * STAGE + (wn * 32 * F + r) * 32;
+    const uint8_t* lxs = lds + 4 * STAGE + (B + wm * 32 * F + r) * 32;
+    auto read_pair = [&](int s, int j, int f) {
+        const int at = (s & 3) * STAGE + ((4 * h + 2 * half + j) ^ ((r >> 1) & 7)) * 16 + f * 4096;
+        a[j][f] = *reinterpret_cast<const i32x4*>(lw + at);
+        b[j][f] = *reinterpret_cast<const i32x4*>(lx + at);
+    };
+    auto read_scales = [&](int s, int set, int f) {
+        const int at = (s >> 2) % 3 * CHUNK + (((s & 3) * 2 + h) ^ (2 * (r >> 3))) * 4 + f * 1024;
+        sw[set][f] = *reinterpret_cast<const int*>(lws + at);
+        sx[set][f] = *reinterpret_cast<const int*>(lxs + at);
+    };
+    f32x16 acc[F][F] = {};
+
+#pragma unroll
+    for (int q = 0; q < 4; ++q) copy_scales(q);
+#pragma unroll
+    for (int s = 0; s < 3; ++s) {
+        copy_stage(s, 0);
+        copy_stage(s, 1);
+        if (s > 0) copy_scales(s + 3);
+    }
+    wait_loads<2 * LOADS>();
+    barrier();
+#pragma unroll
+    for (int f = 0; f < F; ++f) {
+        read_scales(0, 0, f);
+        read_pair(0, 0, f);
+    }
+    for (int s = 0; s < stages; ++s) {
+        wait_loads<LOADS>();  // this wave's copies for the next stage
+        barrier();            // all waves'; and the stage before this one is no longer read
+#pragma unroll
+        for (int f = 0; f < F; ++f) {
+            sw[0][f] >>= 16 * half;
+            sx[0][f] >>= 16 * half;
+        }
+#pragma unroll
+        for (int i = 0; i < F; ++i) {
+            copy_stage(s + 3, i);
+            read_pair(s, 1, i);
+            if (i == F - 1) copy_scales(s + 6);
+#pragma unroll
+            for (int f = 0; f < F; ++f) acc[i][f] = mfma<0>(a[0][f], b[0][i], acc[i][f], sw[0][f], sx[0][i]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+        for (int i = 0; i < F; ++i) {
+            read_pair(s + 1, 0, i);
+            read_scales(s + 1, 1, i);
+#pragma unroll
+            for (int f = 0; f < F; ++f) acc[i][f] = mfma<1>(a[1][f], b[1][i], acc[i][f], sw[0][f], sx[0][i]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+        for (int f = 0; f < F; ++f) {
+            sw[0][f] = sw[1][f];
+            sx[0][f] = sx[1][f];
+        }
+    }
+    wait_loads<0>();  // the copies past the last stage, which wrote zeros
+    barrier();        // and no stage is read any more
+
+    // this group keeps rows 32 half .. + 31 of its waves' 64 and hands the others over
+    float4* mine = reinterpret_cast<float4*>(lds + wave * 8192) + lane;
+    const float4* theirs = reinterpret_cast<const float4*>(lds + (wave ^ 4) * 8192) + lane;
+#pragma unroll
+    for (int f = 0; f < F; ++f)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const f32x16& v = half ? acc[0][f] : acc[1][f];
+            mine[(f * 4 + g) * 64] = make_float4(v[g * 4], v[g * 4 + 1], v[g * 4 + 2], v[g * 4 + 3]);
+        }
+    __syncthreads();
+    f32x16 sum[1][F];
+#pragma unroll
+    for (int f = 0; f < F; ++f)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const float4 t = theirs[(f * 4 + g) * 64];
+            const f32x16& v = half ? acc[1][f] : acc[0][f];
+            sum[0][f][g * 4] = v[g * 4] + t.x;
+            sum[0][f][g * 4 + 1] = v[g * 4 + 1] + t.y;
+            sum[0][f][g * 4 + 2] = v[g * 4 + 2] + t.z;
+            sum[0][f][g * 4 + 3] = v[g * 4 + 3] + t.w;
+        }
+    m0 += wm * 32 * F + half * 32;
+    n0 += wn * 32 * F;
+    auto add_bias = [&](int f, float(&v)[16]) {
+        if (!p.bias) return;
+        float q[16];
+        load_bias(p, n0 + f * 32, q);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[j] += q[j];
+    };
+    MatmulParams out = p;
+    if constexpr (std::is_same<TY, float>::value) out.y = static_cast<float*>(p.y) + split * p.m * p.ldy;
+    write_tile<1, F, TY>(sum, add_bias, out, m0, n0, fast, lds + 65536 + wave * 4096);
+}
+
 // The parts of a split sum, one behind the other -> y.  A thread owns 8 columns.
 template <typename TY>
 __global__ __launch_bounds__(256) void join_kernel(MatmulParams p, const float* __restrict__ parts, int splits,
@@ -428,7 +581,8 @@ template <typename TY>
 void launch_tiles(const MatmulParams& p, bool wide, int splits, int cus, hipStream_t st) {
     const int side = wide ? 256 : 128;
     const int tiles_m = static_cast<int>((p.m + side - 1) / side), tiles_n = (p.n + side - 1) / side;
-    const int stages = (p.kb + 3) / 4, split_stages = splits > 1 ? (stages + 4 * splits - 1) / (4 * splits) * 4 : stages;
+    const int stages = (p.kb + 3) / 4;  // of 128 values; a part has a whole number of chunks of four of 256
+    const int split_stages = splits > 1 ? (stages + 8 * splits - 1) / (8 * splits) * 8 : (stages + 1) / 2 * 2;
     const int parts = (stages + split_stages - 1) / split_stages;
     const Tiling order{tiles_m, tiles_n, parts, split_stages, divisor(tiles_m * tiles_n), divisor(8u * tiles_n),
                        divisor(8), divisor((tiles_m - 1) % 8 + 1)};
@@ -439,13 +593,15 @@ void launch_tiles(const MatmulParams& p, bool wide, int splits, int cus, hipStre
                       (p.ldy * ES % 16 == 0 && reinterpret_cast<uintptr_t>(p.y) % 16 == 0 && p.n <= (1 << 21));
     if (wide)
         wide_kernel<TY><<<static_cast<unsigned>(tiles), 256, 0, st>>>(p, order, fast);
+    else if (tiles <= cus)
+        pair_kernel<TY><<<static_cast<unsigned>(tiles), 512, 0, st>>>(p, order, fast);
     else
         tile_kernel<TY><<<static_cast<unsigned>(tiles < 2 * cus ? tiles : 2 * cus), 256, 0, st>>>(p, order, fast);
 }
 
 // A split sum: parts in fp32 to `work`, then the joining pass.
 void launch_split(const MatmulParams& p, cfwd_dtype y, int splits, int cus, float* work, hipStream_t st) {
-    const int stages = (p.kb + 3) / 4, split_stages = (stages + 4 * splits - 1) / (4 * splits) * 4;
+    const int stages = (p.kb + 3) / 4, split_stages = (stages + 8 * splits - 1) / (8 * splits) * 8;
     const int parts = (stages + split_stages - 1) / split_stages;
     MatmulParams q = p;
     q.bias = nullptr;
@@ -490,16 +646,16 @@ struct Choice {
 
 // The cheapest by a model of the time, in us, fitted to measurements over sums
 // of 2 to 128 stages and 8 to 6000 tiles: a round of tiles takes its stages and
-// an output pass; 128-wide tiles share a CU by twos, or run more than twice as
-// fast alone (narrow and wide: 8192 x 8192 x 8192 420 and 269 us; x 1024: 76 and
+// an output pass; 128-wide tiles share a CU by twos, or have one to themselves
+// (narrow and wide: 8192 x 8192 x 8192 420 and 269 us; x 1024: 76 and
 // 73; x 512: 52 and 59; 25088 x 512 x 256: 13 and 16; 100352 x 1024 x 256: 55 and
 // 85).  A split sum pays for its parts' traffic and a second launch (128 x 1024
-// x 16384: 48 us whole, 19 in 8 parts; 500 x 4096 x 4096: 17 and 26 in 2).
+// x 16384: 33 us whole, 17 in 8 parts; 500 x 4096 x 4096: 14 and 24 in 2).
 Choice choose(const cfwd_mx_matmul_desc* d, int cus) {
     const double stages = static_cast<double>((mx_blocks(d->k) + 3) / 4);
     const long long t2 = (d->m + 127) / 128 * ((d->n + 127) / 128), t4 = (d->m + 255) / 256 * ((d->n + 255) / 256);
     auto rounds = [](long long tiles, long long slots) { return static_cast<double>((tiles + slots - 1) / slots); };
-    const double alone = 0.36, shared = 0.9, wide = 0.82;  // us for 128 values of K
+    const double alone = 0.22, shared = 0.9, wide = 0.82;  // us for 128 values of K
     double best = t2 <= cus ? stages * alone + 2 : rounds(t2, 2 * cus) * (stages * shared + 3.4);
     Choice c{false, 1};
     const double four = rounds(t4, cus) * (stages * wide + 11.5);
@@ -507,7 +663,7 @@ Choice choose(const cfwd_mx_matmul_desc* d, int cus) {
         best = four;
         c = {true, 1};
     }
-    for (int s = 2; s <= 8 && t2 * s <= cus && stages >= 4 * s; s *= 2) {
+    for (int s = 2; s <= 8 && t2 * s <= cus && stages >= 8 * s; s *= 2) {
         const double split = stages / s * alone + 2 + 4 + static_cast<double>(d->m) * d->n * 8 * s / 4e6;
         if (split < best) {
             best = split;

@@ -198,11 +198,11 @@ bool mx_stream_takes_raw(const cfwd_mx_matmul_desc* d) {
            d->x_stride < (1 << 24);
 }
 
-// Beyond 32 rows every workgroup's reading of x counts: the tile kernel then
-// wins unless w is small (48 rows: 4096 x 4096 10.6 us here, 13.4 there; 11000 x
-// 3000 13.8 and 13.1; 4096 x 16384 33 and 22).
+// Beyond 16 rows every workgroup's reading of x counts: tiles then win unless w
+// is small (64 rows: 4096 x 4096 11.9 us here, 12.6 there; 48 rows: 4096 x 16384 33
+// and 18; 17 rows: 16384 x 4096 14.5 and 13.5).
 bool mx_stream_supported(long long m, int n, int k) {
-    return m <= 32 || (m <= 64 && static_cast<long long>(n) * k <= 1 << 24);
+    return m <= 16 || (m <= 64 && static_cast<long long>(n) * k <= 1 << 24);
 }
 
 cfwd_status mx_stream(const mx::MatmulParams& p, cfwd_dtype x, cfwd_dtype y, hipStream_t st) {

@@ -138,6 +138,28 @@ def test_matmul(m, n, k, dtype_y):
     check(x, xt, w, wt, dtype_y, bias=rng.normal(size=n) * 3, act=["relu", "silu", "gelu"][(m + n + k) % 3])
 
 
+@pytest.mark.parametrize("m,n,k", [(2100, 2200, 96), (4100, 2300, 300), (8200, 1030, 70), (2561, 2817, 40),
+                                   (2900, 2900, 3000), (2561, 2817, 2500), (4000, 2600, 2049)])
+@pytest.mark.parametrize("dtype_y", ["f32", "bf16", "mx"])
+def test_matmul_many_tiles(m, n, k, dtype_y):
+    """More tiles than the device holds at once, ragged in both directions, short and long sums (64-bit products on the GPU)."""
+    torch = torch_cuda()
+    rng = np.random.default_rng(m + n + k)
+    say("matmul", m, n, k, dtype_y)
+    x, xt = mx(rng.normal(size=(m, k)) * np.exp(rng.normal(size=(m, 1))))
+    w, wt = mx(rng.normal(size=(n, k)))
+    bias = (rng.normal(size=n) * 3).astype(np.float32)
+    xd, wd, bd = torch.from_numpy(x).cuda(), torch.from_numpy(w).cuda(), torch.from_numpy(bias).cuda()
+    v = (xd @ wd.t() + bd.double()).cpu().numpy()
+    size = (xd.abs() @ wd.abs().t() + bd.double().abs()).cpu().numpy()
+    y, err = R.activate(v, "silu"), 1.2 * (k / 8 + 4) * R.U * size + 2.0 ** -20 * np.abs(v)
+    got = B.mx_matmul(xt, wt, bias=bd, act="silu", out_dtype=dtype_y)
+    if dtype_y == "mx":
+        R.assert_mx_close(got.codes.cpu().numpy(), got.scales.cpu().numpy(), y, err)
+    else:
+        R.assert_close(host(got), y, err, dtype_y == "bf16")
+
+
 @pytest.mark.parametrize("act", ["none", "relu", "silu", "gelu"])
 @pytest.mark.parametrize("m,n,k", [(4, 200, 640), (300, 200, 640)])
 def test_matmul_activations_over_a_wide_range(act, m, n, k):
