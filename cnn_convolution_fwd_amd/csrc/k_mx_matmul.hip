@@ -257,6 +257,182 @@ __global__ __launch_bounds__(256, 2) void tile_kernel(MatmulParams p, Tiling ord
     wait_loads<0>();  // no copy may reach LDS after the workgroup has ended
 }
 
+// Short sums over many rows of y (a 1x1 convolution's shape): 128 x 128 of y as
+// in the narrow kernel, but x is brought to LDS once for all columns of its 128
+// rows, S stages = 128 S values of K, and only w streams through.  A workgroup
+// has a run of tiles in the order of y, columns first.
+//
+// The output pass is most of such a product: its vector instructions (a gelu
+// with its bias and rounding is 9 a value) bound it, and they want waves to
+// change between.  So this kernel keeps its LDS and registers small enough for
+// three workgroups a CU where it can, has no fragments on their way across the
+// barrier, and begins sums with the bias, which travels to LDS with w's scale
+// words (both by waves' own fourth of one copy).
+//
+// 100352 x 1024 x 256, gelu, bf16: 63 us (narrow tiles 76); x in MXFP4 to y in
+// MXFP4, 25088 x 2048 x 512, gelu: 41 (47), without gelu 30 (37).  Quantising x
+// on its way to LDS was slower than a launch of its own before (80 us
+// against 73 with it, 53 against 46), because every workgroup then waits for memory.
+template <int S, typename TY>
+struct Resident {
+    static constexpr int kStage = 128 * 64, kWords = 128 * 8;       // of w: a stage's codes; its scale words and the bias
+    static constexpr bool kThree = S == 2 || std::is_void<TY>::value;  // workgroups a CU, by LDS
+    static constexpr int kRing = S == 2 ? 3 : kThree ? 2 : 4;
+    static constexpr int kW = S * (kStage + 128 * 4), kWS = kW + kRing * kStage, kArea = kWS + kRing * kWords;
+    static constexpr int kBytes = kArea + (std::is_void<TY>::value ? 0 : 8192);
+};
+
+template <int S, typename TY>
+__global__ __launch_bounds__(256, (Resident<S, TY>::kThree ? 3 : 2)) void rows_kernel(MatmulParams p, int tiles_n,
+                                                                                    long long tiles, bool fast) {
+    using L = Resident<S, TY>;
+    constexpr int F = 2, B = 128, STAGE = L::kStage, R = L::kRing, XS = S * STAGE;
+    constexpr int LOADS = 3;  // a wave's copies for a stage of w
+    constexpr int STORES = stores<F, F, TY>();
+    __shared__ __attribute__((aligned(128))) uint8_t lds[L::kBytes];
+    const int lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave >> 1, wn = wave & 1;
+    const int stages = (p.kb + 3) / 4;
+    const long long begin = tiles * blockIdx.x / gridDim.x, end = tiles * (blockIdx.x + 1) / gridDim.x;
+    const uint32_t lds0 = static_cast<uint32_t>(
+        reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t*)lds));
+
+    // copying w: tile's column, stage, place in the ring.  Past the last tile some column is copied that nobody reads.
+    const __amdgpu_buffer_rsrc_t gw = buffer(p.w, static_cast<long long>(p.n) * p.pitch);
+    const __amdgpu_buffer_rsrc_t gs =  // scales (waves 0 and 1) or bias
+        wave < 2 ? buffer(p.ws, static_cast<long long>(p.n) * p.spitch) : buffer(p.bias, p.bias ? p.n * 4ll : 0);
+    const uint32_t column_step = B * p.pitch, column_sstep = wave < 2 ? B * p.spitch : B * 4, stage_sstep = wave < 2 ? 4 : 0;
+    int copy_column = static_cast<int>(begin % tiles_n), copy_stage = 0, copy_slot = 0;
+    const int copy_block = (lane & 3) ^ (lane >> 4);
+    const uint32_t copy_off = (wave * 16 + (lane >> 2)) * p.pitch + copy_block * 16;
+    const uint32_t copy_soff = ((wave & 1) * 64 + lane) * (wave < 2 ? p.spitch : 4);
+    auto copy_codes = [&](int i) {
+        const uint32_t off = copy_off + (copy_column * column_step + copy_stage * 64 + i * 64 * p.pitch);
+        load_to_lds16(gw, copy_stage * 4 + copy_block < p.kb ? off : kOutOfRange,
+                      lds0 + L::kW + copy_slot * STAGE + wave * 1024 + i * 4096);
+    };
+    auto copy_scales = [&] {
+        load_to_lds4(gs, copy_soff + (copy_column * column_sstep + copy_stage * stage_sstep),
+                     lds0 + L::kWS + copy_slot * L::kWords + wave * 256);
+    };
+    auto next_copy = [&] {
+        copy_slot = copy_slot == R - 1 ? 0 : copy_slot + 1;
+        if (++copy_stage < stages) return;
+        copy_stage = 0;
+        copy_column = copy_column == tiles_n - 1 ? 0 : copy_column + 1;
+    };
+
+    // x's rows m0 .. m0 + 127 -> LDS; every wave is done with the rows before
+    auto bring_x = [&](long long m0) {
+        const long long rows = min(static_cast<long long>(B), p.m - m0);
+        const __amdgpu_buffer_rsrc_t gx = buffer(p.x + m0 * p.pitch, rows * p.pitch),
+                                     gxs = buffer(p.xs + m0 * p.spitch, rows * p.spitch);
+#pragma unroll
+        for (int t = 0; t < S; ++t) {
+            const uint32_t off = t * 4 + copy_block < p.kb ? copy_off + t * 64 : kOutOfRange;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) load_to_lds16(gx, off + i * 64 * p.pitch, lds0 + t * STAGE + wave * 1024 + i * 4096);
+        }
+        const int at = lane % S;
+        const uint32_t off = at * 4 < p.spitch ? (wave * (64 / S) + lane / S) * p.spitch + at * 4 : kOutOfRange;
+#pragma unroll
+        for (int i = 0; i < S / 2; ++i)
+            load_to_lds4(gxs, off + i * (256 / S) * p.spitch, lds0 + XS + wave * 256 + i * 1024);
+    };
+
+    const int swz = (r >> 2) & 3;
+    const uint8_t* lw = lds + L::kW + (wn * 32 * F + r) * 64;
+    const uint8_t* lx = lds + (wm * 32 * F + r) * 64;
+    const uint8_t* lws = lds + L::kWS + (wn * 32 * F + r) * 4;
+    const uint8_t* lxs = lds + XS + (wm * 32 * F + r) * (S * 4);
+    const uint8_t* lb = lds + L::kWS + B * 4 + wn * 32 * F * 4 + h * 16;
+
+#pragma unroll
+    for (int s = 0; s < R - 1; ++s) {
+        copy_codes(0);
+        copy_codes(1);
+        copy_scales();
+        next_copy();
+    }
+    int slot = 0, since = R, column = static_cast<int>(begin % tiles_n);
+    long long m_tile = begin / tiles_n;
+    bool fresh = true;  // rows of x to be brought
+    for (long long tile = begin; tile < end; ++tile) {
+        if (fresh) {
+            barrier();
+            bring_x(m_tile * B);
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            wait_loads<0>();  // the first stage's barrier follows
+            fresh = false;
+        }
+        f32x16 acc[F][F];
+        for (int stage = 0; stage < stages; ++stage, ++since) {
+            if (since < R - 1) wait_loads<(R - 2) * LOADS + STORES>();
+            else wait_loads<(R - 2) * LOADS>();
+            barrier();  // this stage of w is whole; the one before is no longer read
+            copy_codes(0);
+            copy_codes(1);
+            copy_scales();
+            next_copy();
+            const uint8_t *w = lw + slot * STAGE, *x = lx + stage * STAGE;
+            i32x4 a[2][F], b[2][F];
+            int sw[F], sx[F];
+#pragma unroll
+            for (int f = 0; f < F; ++f) {
+                sw[f] = *reinterpret_cast<const int*>(lws + slot * L::kWords + f * 128) >> 16 * h;
+                sx[f] = *reinterpret_cast<const int*>(lxs + stage * 4 + f * (S * 128)) >> 16 * h;
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int f = 0; f < F; ++f) {
+                    a[j][f] = *reinterpret_cast<const i32x4*>(w + ((2 * h + j) ^ swz) * 16 + f * 2048);
+                    b[j][f] = *reinterpret_cast<const i32x4*>(x + ((2 * h + j) ^ swz) * 16 + f * 2048);
+                }
+            if (stage == 0) {  // sums begin with the bias
+#pragma unroll
+                for (int f = 0; f < F; ++f)
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        const float4 v = *reinterpret_cast<const float4*>(lb + slot * L::kWords + f * 128 + g * 32);
+#pragma unroll
+                        for (int i = 0; i < F; ++i) {
+                            acc[i][f][g * 4] = v.x;
+                            acc[i][f][g * 4 + 1] = v.y;
+                            acc[i][f][g * 4 + 2] = v.z;
+                            acc[i][f][g * 4 + 3] = v.w;
+                        }
+                    }
+            }
+#pragma unroll
+            for (int i = 0; i < F; ++i)
+#pragma unroll
+                for (int f = 0; f < F; ++f) acc[i][f] = mfma<0>(a[0][f], b[0][i], acc[i][f], sw[f], sx[i]);
+#pragma unroll
+            for (int i = 0; i < F; ++i)
+#pragma unroll
+                for (int f = 0; f < F; ++f) acc[i][f] = mfma<1>(a[1][f], b[1][i], acc[i][f], sw[f], sx[i]);
+            slot = slot == R - 1 ? 0 : slot + 1;
+        }
+        auto no_bias = [](int, float(&)[16]) {};
+        uint8_t* area = nullptr;
+        if constexpr (!std::is_void<TY>::value) {
+            barrier();  // the last stage of w is no longer read
+            area = lds + (wave < 2 ? L::kW + (slot == 0 ? R - 1 : slot - 1) * STAGE + wave * 4096 : L::kArea + (wave - 2) * 4096);
+        }
+        write_tile<F, F, TY>(acc, no_bias, p, m_tile * B + wm * 32 * F, column * B + wn * 32 * F, fast, area);
+        if (!fast) wait_loads<0>();  // an unknown number of stores
+        since = 0;
+        if (++column == tiles_n) {
+            column = 0;
+            ++m_tile;
+            fresh = true;
+        }
+    }
+    wait_loads<0>();  // no copy may reach LDS after the workgroup has ended
+}
+
 // Wide tiles, for long sums over many tiles: 256 rows of y x 256 columns, one
 // tile a workgroup, one workgroup a CU, 128 x 128 a wave: half the copies of the
 // kernel above for the same products.  (256 accumulators a lane leave no
@@ -577,6 +753,14 @@ __global__ __launch_bounds__(256) void join_kernel(MatmulParams p, const float* 
     store_run<TY>(p, row, n, valid, v);
 }
 
+// rows of y are whole 16-byte runs, and a wave's rows within a buffer's 31 bits
+template <typename TY>
+bool whole_runs(const MatmulParams& p) {
+    constexpr int ES = std::is_same<TY, float>::value ? 4 : 2;
+    return std::is_void<TY>::value ||
+           (p.ldy * ES % 16 == 0 && reinterpret_cast<uintptr_t>(p.y) % 16 == 0 && p.n <= (1 << 21));
+}
+
 template <typename TY>
 void launch_tiles(const MatmulParams& p, bool wide, int splits, int cus, hipStream_t st) {
     const int side = wide ? 256 : 128;
@@ -587,16 +771,21 @@ void launch_tiles(const MatmulParams& p, bool wide, int splits, int cus, hipStre
     const Tiling order{tiles_m, tiles_n, parts, split_stages, divisor(tiles_m * tiles_n), divisor(8u * tiles_n),
                        divisor(8), divisor((tiles_m - 1) % 8 + 1)};
     const int tiles = tiles_m * tiles_n * parts;
-    // whole 16-byte runs, and a wave's rows within a buffer's 31 bits
-    constexpr int ES = std::is_same<TY, float>::value ? 4 : 2;
-    const bool fast = std::is_void<TY>::value ||
-                      (p.ldy * ES % 16 == 0 && reinterpret_cast<uintptr_t>(p.y) % 16 == 0 && p.n <= (1 << 21));
+    const bool fast = whole_runs<TY>(p);
     if (wide)
         wide_kernel<TY><<<static_cast<unsigned>(tiles), 256, 0, st>>>(p, order, fast);
     else if (tiles <= cus)
         pair_kernel<TY><<<static_cast<unsigned>(tiles), 512, 0, st>>>(p, order, fast);
     else
         tile_kernel<TY><<<static_cast<unsigned>(tiles < 2 * cus ? tiles : 2 * cus), 256, 0, st>>>(p, order, fast);
+}
+
+template <int S, typename TY>
+void launch_rows(const MatmulParams& p, int cus, hipStream_t st) {
+    const int tiles_n = (p.n + 127) / 128;
+    const long long tiles = (p.m + 127) / 128 * tiles_n;
+    rows_kernel<S, TY><<<static_cast<unsigned>(std::min<long long>(tiles, (Resident<S, TY>::kThree ? 3 : 2) * cus)), 256, 0, st>>>(
+        p, tiles_n, tiles, whole_runs<TY>(p));
 }
 
 // A split sum: parts in fp32 to `work`, then the joining pass.
@@ -642,18 +831,22 @@ int compute_units() {  // of the current device; asked for once
 struct Choice {
     bool wide;
     int splits;
+    bool rows = false;  // x stays in LDS
 };
 
-// The cheapest by a model of the time, in us, fitted to measurements over sums
-// of 2 to 128 stages and 8 to 6000 tiles: a round of tiles takes its stages and
-// an output pass; 128-wide tiles share a CU by twos, or have one to themselves
-// (narrow and wide: 8192 x 8192 x 8192 420 and 269 us; x 1024: 76 and
-// 73; x 512: 52 and 59; 25088 x 512 x 256: 13 and 16; 100352 x 1024 x 256: 55 and
-// 85).  A split sum pays for its parts' traffic and a second launch (128 x 1024
-// x 16384: 33 us whole, 17 in 8 parts; 500 x 4096 x 4096: 14 and 24 in 2).
+// Sums of up to 512 values over more tiles than CUs go to the rows kernel, which
+// was the fastest at every size (narrow, it and wide: 100352 x 128 x 256 13.3,
+// 10.7 and 23 us; 2100 x 2048 x 512 8.7, 7.3 and 13; 8192 x 8192 x 512 48, 38 and
+// 53).  Else the cheapest by a model of the time, in us, fitted to measurements
+// over sums of 2 to 128 stages and 8 to 6000 tiles: a round of tiles takes its
+// stages and an output pass; 128-wide tiles share a CU by twos, or have one to
+// themselves (narrow and wide: 8192 x 8192 x 8192 420 and 269 us; x 1024: 76 and
+// 73).  A split sum pays for its parts' traffic and a second launch (128 x 1024 x
+// 16384: 33 us whole, 17 in 8 parts; 500 x 4096 x 4096: 14 and 24 in 2).
 Choice choose(const cfwd_mx_matmul_desc* d, int cus) {
     const double stages = static_cast<double>((mx_blocks(d->k) + 3) / 4);
     const long long t2 = (d->m + 127) / 128 * ((d->n + 127) / 128), t4 = (d->m + 255) / 256 * ((d->n + 255) / 256);
+    if (stages <= 4 && t2 > cus) return {false, 1, true};
     auto rounds = [](long long tiles, long long slots) { return static_cast<double>((tiles + slots - 1) / slots); };
     const double alone = 0.22, shared = 0.9, wide = 0.82;  // us for 128 values of K
     double best = t2 <= cus ? stages * alone + 2 : rounds(t2, 2 * cus) * (stages * shared + 3.4);
@@ -680,10 +873,9 @@ size_t x_bytes(const cfwd_mx_matmul_desc* d) {  // of an x that the call quantis
 }  // namespace
 
 size_t mx_matmul_workspace(const cfwd_mx_matmul_desc* d) {
-    const bool stream = mx_stream_supported(d->m, d->n, d->k);
-    const size_t x = d->x_dtype == CFWD_MXFP4 || (stream && mx_stream_takes_raw(d)) ? 0 : x_bytes(d);
-    if (stream) return x;
+    if (mx_stream_supported(d->m, d->n, d->k)) return d->x_dtype == CFWD_MXFP4 || mx_stream_takes_raw(d) ? 0 : x_bytes(d);
     const Choice c = choose(d, compute_units());
+    const size_t x = d->x_dtype == CFWD_MXFP4 ? 0 : x_bytes(d);
     return x + (c.splits > 1 ? static_cast<size_t>(c.splits) * d->m * ((d->n + 3) / 4 * 4) * 4 : 0);
 }
 
@@ -693,6 +885,8 @@ cfwd_status mx_matmul(const cfwd_mx_matmul_desc* d, const void* x, const void* x
     mx::MatmulParams p{};
     uint8_t* work = static_cast<uint8_t*>(workspace);
     const bool stream = mx_stream_supported(d->m, d->n, d->k);
+    const int cus = compute_units();
+    const Choice c = stream ? Choice{} : choose(d, cus);
     const bool raw = d->x_dtype != CFWD_MXFP4 && stream && mx_stream_takes_raw(d);
     if (d->x_dtype != CFWD_MXFP4 && !raw) {
         uint8_t* scales = work + round256(static_cast<size_t>(d->m) * mx_code_pitch(d->k));
@@ -721,9 +915,14 @@ cfwd_status mx_matmul(const cfwd_mx_matmul_desc* d, const void* x, const void* x
     p.y_pitch = static_cast<int>(mx_code_pitch(d->n));
     p.y_spitch = static_cast<int>(mx_scale_pitch(d->n));
     if (stream) return mx_stream(p, raw ? d->x_dtype : CFWD_MXFP4, d->y_dtype, st);
-    const int cus = compute_units();
-    const Choice c = choose(d, cus);
-    if (c.splits > 1)
+    const bool half = p.kb <= 8;  // of what the rows kernel can hold
+    if (c.rows && d->y_dtype == CFWD_F32)
+        half ? mx::launch_rows<2, float>(p, cus, st) : mx::launch_rows<4, float>(p, cus, st);
+    else if (c.rows && d->y_dtype == CFWD_BF16)
+        half ? mx::launch_rows<2, bf16_t>(p, cus, st) : mx::launch_rows<4, bf16_t>(p, cus, st);
+    else if (c.rows)
+        half ? mx::launch_rows<2, void>(p, cus, st) : mx::launch_rows<4, void>(p, cus, st);
+    else if (c.splits > 1)
         mx::launch_split(p, d->y_dtype, c.splits, cus, reinterpret_cast<float*>(work), st);
     else if (d->y_dtype == CFWD_F32)
         mx::launch_tiles<float>(p, c.wide, 1, cus, st);

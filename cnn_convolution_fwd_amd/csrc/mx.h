@@ -178,11 +178,13 @@ __device__ __forceinline__ uint32_t quantize8(const float (&v)[8], uint32_t* byt
 // Activations in fp32.  NaN stays NaN.  silu(v) = v / (1 + e^-v); gelu is the
 // form with tanh, 0.5 v (1 + tanh z) = v / (1 + e^-2z), z = sqrt(2 / pi) (v +
 // 0.044715 v^3); the powers of 2 are taken directly, with log2(e) in the constants.
+__device__ __forceinline__ float silu_exponent(float v) { return -1.44269504f * v; }
+__device__ __forceinline__ float gelu_exponent(float v) { return v * (-2.30220820f - 0.10294324f * (v * v)); }
+
 __device__ __forceinline__ float activate(float v, int act) {
     if (act == CFWD_ACT_RELU) return v < 0.0f ? 0.0f : v;
-    if (act == CFWD_ACT_SILU) return v * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504f * v));
-    if (act == CFWD_ACT_GELU)
-        return v * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(v * (-2.30220820f - 0.10294324f * (v * v))));
+    if (act == CFWD_ACT_SILU) return v * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(silu_exponent(v)));
+    if (act == CFWD_ACT_GELU) return v * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(gelu_exponent(v)));
     return v;
 }
 

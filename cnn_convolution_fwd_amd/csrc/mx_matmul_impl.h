@@ -92,17 +92,40 @@ constexpr int stores() {
     return std::is_void<TY>::value ? FM * FN : FM * FN * (std::is_same<TY, float>::value ? 4 : 2);
 }
 
+// v / (1 + 2^arg(v)), eight values at a time and step by step: a value's
+// exponential and reciprocal, one right after the other, would each hold up the
+// instruction that takes it.
+template <typename Arg>
+__device__ __forceinline__ void logistic16(float (&v)[16], Arg arg) {
+#pragma unroll
+    for (int g = 0; g < 16; g += 8) {
+        float t[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) t[i] = arg(v[g + i]);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) t[i] = __builtin_amdgcn_exp2f(t[i]);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) t[i] = 1.0f + t[i];
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) t[i] = __builtin_amdgcn_rcpf(t[i]);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[g + i] *= t[i];
+    }
+}
+
 __device__ __forceinline__ void activate16(float (&v)[16], int act) {
     if (act == CFWD_ACT_NONE) return;
     if (act == CFWD_ACT_RELU) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) v[i] = activate(v[i], CFWD_ACT_RELU);
     } else if (act == CFWD_ACT_SILU) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = activate(v[i], CFWD_ACT_SILU);
+        logistic16(v, silu_exponent);
     } else {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = activate(v[i], CFWD_ACT_GELU);
+        logistic16(v, gelu_exponent);
     }
 }
 
@@ -127,9 +150,9 @@ __device__ __forceinline__ void load_bias(const MatmulParams& p, int n, float (&
 template <int FM, int FN, typename TY, typename Bias>
 __device__ __forceinline__ void write_tile(const f32x16 (&acc)[FM][FN], Bias add_bias, const MatmulParams& p,
                                            long long m0, int n0, bool fast, uint8_t* area) {
-    int lane = threadIdx.x & 63;
+    uint32_t lane = threadIdx.x & 63;
     asm volatile("" : "+v"(lane));  // keeps the pass's many addresses from being computed, and held, outside the caller's loop
-    const int r = lane & 31, h = lane >> 5;
+    const uint32_t r = lane & 31, h = (lane >> 5) & 1;
     const long long rows = min(32ll * FM, p.m - m0);
     if constexpr (!std::is_void<TY>::value) {
         constexpr int ES = sizeof(TY), CF = ES == 4 ? FN / 2 : FN;  // columns' fragments of one turn
@@ -138,10 +161,11 @@ __device__ __forceinline__ void write_tile(const f32x16 (&acc)[FM][FN], Bias add
         const long long pitch = static_cast<long long>(p.ldy) * ES;
         uint8_t* y0 = static_cast<uint8_t*>(p.y) + m0 * pitch + static_cast<long long>(n0) * ES;
         const __amdgpu_buffer_rsrc_t y = buffer(y0, (rows - 1) * pitch + (static_cast<long long>(p.ldy) - n0) * ES);
-        const int row0 = lane / SLOTS, slot = lane % SLOTS;
-        auto place = [](int row, int at) { return at ^ ((SLOTS > 8 ? row : row >> 1) & (SLOTS - 1)); };
+        const uint32_t row0 = lane / SLOTS, slot = lane % SLOTS;
+        auto turned = [](uint32_t row) { return ((SLOTS > 8 ? row : row >> 1) & (SLOTS - 1)) * 16; };
+        const uint32_t put = r * ROW + (turned(r) ^ (ES == 4 ? h * 16 : 0)) + (ES == 4 ? 0 : h * 8);
         auto store_turn = [&](int i, int f0, const u32x4(&t)[RUNS]) {
-            const int c = f0 * 32 + slot * RUN, valid = p.n - n0 - c;
+            const int c = f0 * 32 + static_cast<int>(slot) * RUN, valid = p.n - n0 - c;
             if (fast) {
                 const uint32_t off = valid > 0 ? row0 * static_cast<uint32_t>(pitch) + c * ES : kOutOfRange;
 #pragma unroll
@@ -151,7 +175,7 @@ __device__ __forceinline__ void write_tile(const f32x16 (&acc)[FM][FN], Bias add
             }
 #pragma unroll
             for (int u = 0; u < RUNS; ++u) {
-                const int row = i * 32 + u * STEP + row0;
+                const int row = i * 32 + u * STEP + static_cast<int>(row0);
                 if (row >= rows || valid <= 0) continue;
                 TY* dst = reinterpret_cast<TY*>(y0 + row * pitch) + c;
                 if (valid >= RUN) {
@@ -181,8 +205,7 @@ __device__ __forceinline__ void write_tile(const f32x16 (&acc)[FM][FN], Bias add
                     activate16(v, p.act);
 #pragma unroll
                     for (int g = 0; g < 4; ++g) {
-                        const int byte = (f * 32 + g * 8 + h * 4) * ES;
-                        uint8_t* at = area + r * ROW + place(r, byte / 16) * 16 + byte % 16;
+                        uint8_t* at = area + (put ^ static_cast<uint32_t>((f * 32 + g * 8) * ES));
                         if constexpr (ES == 4)
                             *reinterpret_cast<float4*>(at) = make_float4(v[g * 4], v[g * 4 + 1], v[g * 4 + 2], v[g * 4 + 3]);
                         else
@@ -194,8 +217,8 @@ __device__ __forceinline__ void write_tile(const f32x16 (&acc)[FM][FN], Bias add
                 u32x4 t[RUNS];
 #pragma unroll
                 for (int u = 0; u < RUNS; ++u) {
-                    const int row = u * STEP + row0;
-                    t[u] = *reinterpret_cast<const u32x4*>(area + row * ROW + place(row, slot) * 16);
+                    const uint32_t row = u * STEP + row0;
+                    t[u] = *reinterpret_cast<const u32x4*>(area + (row * ROW + (turned(row) ^ slot * 16)));
                 }
                 wave_sync();
                 store_turn(i, f0, t);
@@ -218,7 +241,7 @@ __device__ __forceinline__ void write_tile(const f32x16 (&acc)[FM][FN], Bias add
                     activate16(v, p.act);
                     if (nb + 32 > p.n) {  // columns past the row are no part of its last block
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) v[j] = nb + j / 4 * 8 + h * 4 + j % 4 < p.n ? v[j] : 0.0f;
+                        for (int j = 0; j < 16; ++j) v[j] = nb + j / 4 * 8 + static_cast<int>(h) * 4 + j % 4 < p.n ? v[j] : 0.0f;
                     }
                     uint32_t top = 0;
 #pragma unroll
@@ -245,7 +268,7 @@ __device__ __forceinline__ void write_tile(const f32x16 (&acc)[FM][FN], Bias add
                     block[2 * t + 1] = __builtin_amdgcn_perm(x[1], x[0], 0x07060302u);
                 }
                 __builtin_amdgcn_sched_barrier(0);  // no register holds more than one turn's results
-                const int nb = n0 / 32 + f0 + h;    // rows past the end are out of the buffers' range
+                const int nb = n0 / 32 + f0 + static_cast<int>(h);    // rows past the end are out of the buffers' range
                 const uint32_t off = nb * 16 < p.y_pitch ? r * p.y_pitch + nb * 16 : kOutOfRange;
                 const uint32_t soff = nb < p.y_spitch ? r * p.y_spitch + nb : kOutOfRange;
                 __builtin_amdgcn_raw_buffer_store_b128(block, y, off + i * 32 * p.y_pitch, 0, 0);
