@@ -87,30 +87,29 @@ __global__ __launch_bounds__(256, 2) void tile_kernel(MatmulParams p, Tiling ord
     const int wm = wave >> 1, wn = wave & 1;
 
     // The i-th tile of this workgroup.  A round of tiles is a run of their order, each XCD a run within it.
-    const int tiles = order.tiles.d * order.splits;
+    const int tiles = order.tiles.d;
     const int rounds = (tiles - 1 - static_cast<int>(blockIdx.x)) / static_cast<int>(gridDim.x) + 1;
-    auto tile_at = [&](int i, long long* m0, int* n0, int* split) {
+    auto tile_at = [&](int i, long long* m0, int* n0) {
         const int first = i * gridDim.x;
-        tile_place<B>(order, first + xcd_linear(blockIdx.x, min(static_cast<int>(gridDim.x), tiles - first)), m0, n0, split);
+        int split;  // there is one part
+        tile_place<B>(order, first + xcd_linear(blockIdx.x, min(static_cast<int>(gridDim.x), tiles - first)), m0, n0, &split);
     };
 
-    const int all_stages = (p.kb + 3) / 4;
-    auto stages_of = [&](int split) { return min(order.split_stages, all_stages - split * order.split_stages); };
+    const int stages = (p.kb + 3) / 4;
     const uint32_t lds0 = static_cast<uint32_t>(
         reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t*)lds));
-    // copying: tile number, stage of K and the tile's end, stage and group of all
-    int copy_tile = 0, copy_stage = 0, copy_end = 0, copy_count = 0, copy_group = 0;
+    // copying: tile number, stage of K, stage and group of all
+    int copy_tile = 0, copy_stage = 0, copy_count = 0, copy_group = 0;
     __amdgpu_buffer_rsrc_t gx, gxs, gw, gws;
     auto open_tile = [&] {
         long long m0 = 0, rows_x = 0, rows_w = 0;
-        int n0 = 0, split = 0;
+        int n0 = 0;
         if (copy_tile < rounds) {
-            tile_at(copy_tile, &m0, &n0, &split);
+            tile_at(copy_tile, &m0, &n0);
             rows_x = min(static_cast<long long>(B), p.m - m0);
             rows_w = min(B, p.n - n0);
         }
-        copy_stage = split * order.split_stages;  // a whole number of groups
-        copy_end = copy_stage + stages_of(split);
+        copy_stage = 0;
         gx = buffer(p.x + m0 * p.pitch, rows_x * p.pitch);
         gxs = buffer(p.xs + m0 * p.spitch, rows_x * p.spitch);
         gw = buffer(p.w + static_cast<long long>(n0) * p.pitch, rows_w * p.pitch);
@@ -137,8 +136,8 @@ __global__ __launch_bounds__(256, 2) void tile_kernel(MatmulParams p, Tiling ord
     };
     auto next_copy = [&] {
         ++copy_count;
-        if ((++copy_stage & 3) == 0 || copy_stage == copy_end) ++copy_group;
-        if (copy_stage == copy_end) {
+        if ((++copy_stage & 3) == 0 || copy_stage == stages) ++copy_group;
+        if (copy_stage == stages) {
             ++copy_tile;
             open_tile();
         }
@@ -186,16 +185,12 @@ __global__ __launch_bounds__(256, 2) void tile_kernel(MatmulParams p, Tiling ord
     int since = 4;             // stages since the last output pass
     for (int tile = 0; tile < rounds; ++tile) {
         long long m0;
-        int n0, split;
-        tile_at(tile, &m0, &n0, &split);
-        const int stages = stages_of(split);
+        int n0;
+        tile_at(tile, &m0, &n0);
         m0 += wm * 32 * F;
         n0 += wn * 32 * F;
         float bias[F][16];
-        if (p.bias) {  // requested ahead of the output pass
-#pragma unroll
-            for (int f = 0; f < F; ++f) load_bias(p, n0 + f * 32, bias[f]);
-        }
+        load_bias(p, n0, bias);  // ahead of the output pass
         for (int stage = 0; stage < stages; ++stage, ++count, ++since) {
             // This wave's copies for the next stage: those for the one after it, and stores, may be outstanding.
             if (since < 2) {
@@ -239,14 +234,13 @@ __global__ __launch_bounds__(256, 2) void tile_kernel(MatmulParams p, Tiling ord
             }
         }
         barrier();  // the last stage's LDS is no longer read
-        auto add_bias = [&](int f, float(&v)[16]) {
-            if (!p.bias) return;
 #pragma unroll
-            for (int j = 0; j < 16; ++j) v[j] += bias[f][j];
-        };
-        MatmulParams part = p;
-        if constexpr (std::is_same<TY, float>::value) part.y = static_cast<float*>(p.y) + split * p.m * p.ldy;
-        write_tile<F, F, TY>(acc, add_bias, part, m0, n0, fast, lds + ((count - 1) & 3) * STAGE + wave * (STAGE / 4));
+        for (int i = 0; i < F; ++i)
+#pragma unroll
+            for (int f = 0; f < F; ++f)
+#pragma unroll
+                for (int j = 0; j < 16; ++j) acc[i][f][j] += bias[f][j];
+        write_tile<F, F, TY>(acc, p, m0, n0, fast, lds + ((count - 1) & 3) * STAGE + wave * (STAGE / 4));
         if (!fast) wait_loads<0>();  // an unknown number of stores
 #pragma unroll
         for (int i = 0; i < F; ++i)
@@ -415,13 +409,12 @@ __global__ __launch_bounds__(256, (Resident<S, TY>::kThree ? 3 : 2)) void rows_k
                 for (int f = 0; f < F; ++f) acc[i][f] = mfma<1>(a[1][f], b[1][i], acc[i][f], sw[f], sx[i]);
             slot = slot == R - 1 ? 0 : slot + 1;
         }
-        auto no_bias = [](int, float(&)[16]) {};
         uint8_t* area = nullptr;
         if constexpr (!std::is_void<TY>::value) {
             barrier();  // the last stage of w is no longer read
             area = lds + (wave < 2 ? L::kW + (slot == 0 ? R - 1 : slot - 1) * STAGE + wave * 4096 : L::kArea + (wave - 2) * 4096);
         }
-        write_tile<F, F, TY>(acc, no_bias, p, m_tile * B + wm * 32 * F, column * B + wn * 32 * F, fast, area);
+        write_tile<F, F, TY>(acc, p, m_tile * B + wm * 32 * F, column * B + wn * 32 * F, fast, area);
         if (!fast) wait_loads<0>();  // an unknown number of stores
         since = 0;
         if (++column == tiles_n) {
@@ -503,7 +496,7 @@ __global__ __launch_bounds__(256, 1) void wide_kernel(MatmulParams p, Tiling ord
         sw[set][f] = *reinterpret_cast<const int*>(lws + at);
         sx[set][f] = *reinterpret_cast<const int*>(lxs + at);
     };
-    f32x16 acc[F][F] = {};
+    f32x16 acc[F][F];
     auto multiply = [&](auto j, int i) {
         constexpr int J = decltype(j)::value;
 #pragma unroll
@@ -517,6 +510,16 @@ __global__ __launch_bounds__(256, 1) void wide_kernel(MatmulParams p, Tiling ord
     for (int q = 0; q < 5; ++q)
 #pragma unroll
         for (int i = 0; i < 4; ++i) copy_scales(q, i);
+    {  // sums begin with the bias
+        float bias[F][16];
+        load_bias(p, n0 + wn * 32 * F, bias);
+#pragma unroll
+        for (int i = 0; i < F; ++i)
+#pragma unroll
+            for (int f = 0; f < F; ++f)
+#pragma unroll
+                for (int j = 0; j < 16; ++j) acc[i][f][j] = bias[f][j];
+    }
     wait_loads<0>();
 #pragma unroll
     for (int i = 0; i < 4; ++i) copy_codes(1, i);
@@ -564,14 +567,7 @@ __global__ __launch_bounds__(256, 1) void wide_kernel(MatmulParams p, Tiling ord
     barrier();
     m0 += wm * 32 * F;
     n0 += wn * 32 * F;
-    auto add_bias = [&](int f, float(&v)[16]) {
-        if (!p.bias) return;
-        float q[16];
-        load_bias(p, n0 + f * 32, q);
-#pragma unroll
-        for (int j = 0; j < 16; ++j) v[j] += q[j];
-    };
-    write_tile<F, F, TY>(acc, add_bias, p, m0, n0, fast, lds + wave * (STAGE / 4));
+    write_tile<F, F, TY>(acc, p, m0, n0, fast, lds + wave * (STAGE / 4));
 }
 
 // Few tiles, no more than CUs: 128 x 128 of y, or of one part of a split sum, a
@@ -639,6 +635,8 @@ __global__ __launch_bounds__(512, 1) void pair_kernel(MatmulParams p, Tiling ord
         sw[set][f] = *reinterpret_cast<const int*>(lws + at);
         sx[set][f] = *reinterpret_cast<const int*>(lxs + at);
     };
+    float bias[F][16];
+    load_bias(p, n0 + wn * 32 * F, bias);  // ahead of the output pass
     f32x16 acc[F][F] = {};
 
 #pragma unroll
@@ -708,23 +706,16 @@ __global__ __launch_bounds__(512, 1) void pair_kernel(MatmulParams p, Tiling ord
         for (int g = 0; g < 4; ++g) {
             const float4 t = theirs[(f * 4 + g) * 64];
             const f32x16& v = half ? acc[1][f] : acc[0][f];
-            sum[0][f][g * 4] = v[g * 4] + t.x;
-            sum[0][f][g * 4 + 1] = v[g * 4 + 1] + t.y;
-            sum[0][f][g * 4 + 2] = v[g * 4 + 2] + t.z;
-            sum[0][f][g * 4 + 3] = v[g * 4 + 3] + t.w;
+            sum[0][f][g * 4] = v[g * 4] + t.x + bias[f][g * 4];
+            sum[0][f][g * 4 + 1] = v[g * 4 + 1] + t.y + bias[f][g * 4 + 1];
+            sum[0][f][g * 4 + 2] = v[g * 4 + 2] + t.z + bias[f][g * 4 + 2];
+            sum[0][f][g * 4 + 3] = v[g * 4 + 3] + t.w + bias[f][g * 4 + 3];
         }
     m0 += wm * 32 * F + half * 32;
     n0 += wn * 32 * F;
-    auto add_bias = [&](int f, float(&v)[16]) {
-        if (!p.bias) return;
-        float q[16];
-        load_bias(p, n0 + f * 32, q);
-#pragma unroll
-        for (int j = 0; j < 16; ++j) v[j] += q[j];
-    };
     MatmulParams out = p;
     if constexpr (std::is_same<TY, float>::value) out.y = static_cast<float*>(p.y) + split * p.m * p.ldy;
-    write_tile<1, F, TY>(sum, add_bias, out, m0, n0, fast, lds + 65536 + wave * 4096);
+    write_tile<1, F, TY>(sum, out, m0, n0, fast, lds + 65536 + wave * 4096);
 }
 
 // The parts of a split sum, one behind the other -> y.  A thread owns 8 columns.

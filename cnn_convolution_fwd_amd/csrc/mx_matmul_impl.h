@@ -6,10 +6,11 @@
 // bytes) of row lane % 32 of each, with the block's scale byte, and ends with
 // 16 outputs of one row of y: columns 8 g + 4 h + i (g, i < 4) of 32.
 //
-// A stage is 256 values of K, 8 blocks, as four such instructions.  The order
-// of the sum is free as long as both operands agree, so half h takes the
-// stage's blocks 4 h .. 4 h + 3, one an instruction: their four scale bytes are
-// then one aligned word, and each instruction names its byte.
+// A stage is 256 values of K, 8 blocks, as four such instructions, or half of
+// that.  The order of the sum is free as long as both operands agree, so half h
+// takes the stage's blocks 4 h .. 4 h + 3 (or 2 h and 2 h + 1), one an
+// instruction: their scale bytes are then in one aligned word, and each
+// instruction names its byte.
 #pragma once
 
 #include "mx.h"
@@ -75,8 +76,7 @@ __device__ __forceinline__ void store_run(const MatmulParams& p, long long row, 
 }
 
 // The output pass of one wave: 32 FM rows of y x 32 FN columns from (m0, n0)
-// on, with bias (add_bias(f, v) adds that of columns' fragment f), activation
-// and the one rounding.
+// on, with activation and the one rounding.
 //
 // fp32 and bf16 results take a turn through the wave's own LDS area (32 rows, of
 // one or half a set of columns' fragments; 16-byte slots permuted by row instead
@@ -135,21 +135,24 @@ __device__ __forceinline__ void wave_sync() {  // a wave's LDS writes before its
     __builtin_amdgcn_sched_barrier(0);  // and no register holds more than one turn's results
 }
 
-// bias of a lane's 16 columns of the 32 from n on
-__device__ __forceinline__ void load_bias(const MatmulParams& p, int n, float (&v)[16]) {
-    const __amdgpu_buffer_rsrc_t b = buffer(p.bias, p.n * 4ll);
+// bias of a lane's columns of the 32 F from n on; 0 if there is none
+template <int F>
+__device__ __forceinline__ void load_bias(const MatmulParams& p, int n, float (&v)[F][16]) {
+    const __amdgpu_buffer_rsrc_t b = buffer(p.bias, p.bias ? p.n * 4ll : 0);
     const int h = (threadIdx.x >> 5) & 1;
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-        const u32x4 q = __builtin_amdgcn_raw_buffer_load_b128(b, (n + g * 8 + h * 4) * 4, 0, 0);
+    for (int f = 0; f < F; ++f)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[g * 4 + i] = __uint_as_float(q[i]);
-    }
+        for (int g = 0; g < 4; ++g) {
+            const u32x4 q = __builtin_amdgcn_raw_buffer_load_b128(b, (n + f * 32 + g * 8 + h * 4) * 4, 0, 0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[f][g * 4 + i] = __uint_as_float(q[i]);
+        }
 }
 
-template <int FM, int FN, typename TY, typename Bias>
-__device__ __forceinline__ void write_tile(const f32x16 (&acc)[FM][FN], Bias add_bias, const MatmulParams& p,
-                                           long long m0, int n0, bool fast, uint8_t* area) {
+template <int FM, int FN, typename TY>
+__device__ __forceinline__ void write_tile(const f32x16 (&acc)[FM][FN], const MatmulParams& p, long long m0, int n0, bool fast,
+                                           uint8_t* area) {
     uint32_t lane = threadIdx.x & 63;
     asm volatile("" : "+v"(lane));  // keeps the pass's many addresses from being computed, and held, outside the caller's loop
     const uint32_t r = lane & 31, h = (lane >> 5) & 1;
@@ -192,37 +195,38 @@ __device__ __forceinline__ void write_tile(const f32x16 (&acc)[FM][FN], Bias add
                     }
             }
         };
+        // a turn's results come back from LDS while the next turn's are computed
+        constexpr int TURNS = FM * (FN / CF);
+        u32x4 t[RUNS];
 #pragma unroll
-        for (int i = 0; i < FM; ++i)
+        for (int turn = 0; turn < TURNS; ++turn) {
+            const int i = turn / (FN / CF), f0 = turn % (FN / CF) * CF;
 #pragma unroll
-            for (int f0 = 0; f0 < FN; f0 += CF) {
+            for (int f = 0; f < CF; ++f) {
+                float v[16];
 #pragma unroll
-                for (int f = 0; f < CF; ++f) {
-                    float v[16];
+                for (int j = 0; j < 16; ++j) v[j] = acc[i][f0 + f][j];
+                activate16(v, p.act);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) v[j] = acc[i][f0 + f][j];
-                    add_bias(f0 + f, v);
-                    activate16(v, p.act);
-#pragma unroll
-                    for (int g = 0; g < 4; ++g) {
-                        uint8_t* at = area + (put ^ static_cast<uint32_t>((f * 32 + g * 8) * ES));
-                        if constexpr (ES == 4)
-                            *reinterpret_cast<float4*>(at) = make_float4(v[g * 4], v[g * 4 + 1], v[g * 4 + 2], v[g * 4 + 3]);
-                        else
-                            *reinterpret_cast<uint2*>(at) =
-                                make_uint2(pack_bf16x2(v[g * 4], v[g * 4 + 1]), pack_bf16x2(v[g * 4 + 2], v[g * 4 + 3]));
-                    }
+                for (int g = 0; g < 4; ++g) {
+                    uint8_t* at = area + (put ^ static_cast<uint32_t>((f * 32 + g * 8) * ES));
+                    if constexpr (ES == 4)
+                        *reinterpret_cast<float4*>(at) = make_float4(v[g * 4], v[g * 4 + 1], v[g * 4 + 2], v[g * 4 + 3]);
+                    else
+                        *reinterpret_cast<uint2*>(at) =
+                            make_uint2(pack_bf16x2(v[g * 4], v[g * 4 + 1]), pack_bf16x2(v[g * 4 + 2], v[g * 4 + 3]));
                 }
-                wave_sync();
-                u32x4 t[RUNS];
-#pragma unroll
-                for (int u = 0; u < RUNS; ++u) {
-                    const uint32_t row = u * STEP + row0;
-                    t[u] = *reinterpret_cast<const u32x4*>(area + (row * ROW + (turned(row) ^ slot * 16)));
-                }
-                wave_sync();
-                store_turn(i, f0, t);
             }
+            wave_sync();
+            if (turn > 0) store_turn((turn - 1) / (FN / CF), (turn - 1) % (FN / CF) * CF, t);
+#pragma unroll
+            for (int u = 0; u < RUNS; ++u) {
+                const uint32_t row = u * STEP + row0;
+                t[u] = *reinterpret_cast<const u32x4*>(area + (row * ROW + (turned(row) ^ slot * 16)));
+            }
+            wave_sync();
+        }
+        store_turn(FM - 1, FN - CF, t);
     } else {
         const __amdgpu_buffer_rsrc_t y = buffer(static_cast<uint8_t*>(p.y) + m0 * p.y_pitch, rows * p.y_pitch),
                                      ys = buffer(p.ys + m0 * p.y_spitch, rows * p.y_spitch);
@@ -237,15 +241,21 @@ __device__ __forceinline__ void write_tile(const f32x16 (&acc)[FM][FN], Bias add
                     float v[16];
 #pragma unroll
                     for (int j = 0; j < 16; ++j) v[j] = acc[i][f0 + q][j];
-                    add_bias(f0 + q, v);
                     activate16(v, p.act);
                     if (nb + 32 > p.n) {  // columns past the row are no part of its last block
 #pragma unroll
                         for (int j = 0; j < 16; ++j) v[j] = nb + j / 4 * 8 + static_cast<int>(h) * 4 + j % 4 < p.n ? v[j] : 0.0f;
                     }
-                    uint32_t top = 0;
+                    // the largest |v|: the largest of v's bits as signed numbers is that of the positive values if there
+                    // are any, as unsigned ones that of the negative values; without their signs the greater of the two
+                    int most = static_cast<int>(__float_as_uint(v[0]));
+                    uint32_t top = __float_as_uint(v[0]);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) top = max(top, abs_bits(v[j]));
+                    for (int j = 1; j < 16; ++j) {
+                        most = max(most, static_cast<int>(__float_as_uint(v[j])));
+                        top = max(top, __float_as_uint(v[j]));
+                    }
+                    top = max(top & 0x7fffffffu, static_cast<uint32_t>(most) & 0x7fffffffu);
                     top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 32)));
                     byte[q] = nb < p.n ? exponent_byte(top) : 127u;
                     const float s = scale_of(byte[q]);
