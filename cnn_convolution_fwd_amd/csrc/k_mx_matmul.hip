@@ -38,16 +38,16 @@ struct Tiling {
     Divisor group, height, last_height;  // of tiles in a group of 8 rows of tiles; of rows in a group, in the last one
 };
 
-// The u-th tile, of BxB: the order goes down columns of 8 tiles, part by part.
-template <int B>
+// The u-th tile, of BM x BN: the order goes down columns of 8 tiles, part by part.
+template <int BM, int BN>
 __device__ __forceinline__ void tile_place(const Tiling& order, int u, long long* m0, int* n0, int* split) {
     *split = divide(u, order.tiles);
     const int t = u - *split * order.tiles.d;
     const int group = divide(t, order.group), in_group = t - group * order.group.d;
     const Divisor height = group == (order.tiles_m - 1) / 8 ? order.last_height : order.height;
     const int column = divide(in_group, height);
-    *m0 = static_cast<long long>(group * 8 + in_group - column * height.d) * B;
-    *n0 = column * B;
+    *m0 = static_cast<long long>(group * 8 + in_group - column * height.d) * BM;
+    *n0 = column * BN;
 }
 
 // Tiles through LDS: 128 rows of y x 128 columns; the four waves (2 x 2) of a
@@ -92,7 +92,7 @@ __global__ __launch_bounds__(256, 2) void tile_kernel(MatmulParams p, Tiling ord
     auto tile_at = [&](int i, long long* m0, int* n0) {
         const int first = i * gridDim.x;
         int split;  // there is one part
-        tile_place<B>(order, first + xcd_linear(blockIdx.x, min(static_cast<int>(gridDim.x), tiles - first)), m0, n0, &split);
+        tile_place<B, B>(order, first + xcd_linear(blockIdx.x, min(static_cast<int>(gridDim.x), tiles - first)), m0, n0, &split);
     };
 
     const int stages = (p.kb + 3) / 4;
@@ -453,7 +453,7 @@ __global__ __launch_bounds__(256, 1) void wide_kernel(MatmulParams p, Tiling ord
     const int wm = wave >> 1, wn = wave & 1;
     long long m0;
     int n0, split;
-    tile_place<B>(order, xcd_linear(blockIdx.x, gridDim.x), &m0, &n0, &split);
+    tile_place<B, B>(order, xcd_linear(blockIdx.x, gridDim.x), &m0, &n0, &split);
     const int stages = (p.kb + 7) / 8;
     const long long rows_x = min(static_cast<long long>(B), p.m - m0), rows_w = min(B, p.n - n0);
     const __amdgpu_buffer_rsrc_t gx = buffer(p.x + m0 * p.pitch, rows_x * p.pitch),
@@ -570,30 +570,33 @@ __global__ __launch_bounds__(256, 1) void wide_kernel(MatmulParams p, Tiling ord
     write_tile<F, F, TY>(acc, p, m0, n0, fast, lds + wave * (STAGE / 4));
 }
 
-// Few tiles, no more than CUs: 128 x 128 of y, or of one part of a split sum, a
-// workgroup, alone on its CU.  Two groups of four waves share each stage's
-// products: group g takes steps 2 g and 2 g + 1, so every SIMD has two waves to
-// alternate between, and the groups' sums meet in LDS at the end, each group
-// finishing half of each wave's rows (500 x 4096 x 4096: 13.7 us, 17.6 with the
-// narrow kernel; 2048 x 2048 x 8192: 26 and 34).
+// Few tiles, no more than CUs: 128 columns of y x 128 rows, or x 64 where those
+// are still no more than CUs (of y, or of one part of a split sum), a workgroup,
+// alone on its CU.  Two groups of four waves share each stage's products: group
+// g takes steps 2 g and 2 g + 1, so every SIMD has two waves to alternate
+// between, and the groups' sums meet in LDS at the end, each group finishing
+// half of each wave's rows (2048 x 2048 x 8192: 26 us, 34 with the narrow kernel;
+// 500 x 4096 x 4096 by 64 rows 12.0, by 128 13.5, narrow 17.6).  A fifth stage in
+// LDS gained nothing: memory's latency is not what bounds it, but a CU's rate
+// of copies to LDS and the chain from a stage's barrier to the next.
 //
 // A stage is 256 values of K (whole cache lines, rows and slots as in the wide
 // kernel); LDS holds four, used as by the narrow kernel: s is multiplied, s + 1
 // is whole, s + 2 on its way, s + 3 requested.  Scales come in chunks of four
 // stages, a quarter with each stage's copies, into three areas in turn.
-template <typename TY>
+template <int FM, typename TY>
 __global__ __launch_bounds__(512, 1) void pair_kernel(MatmulParams p, Tiling order, bool fast) {
-    constexpr int F = 2, B = 64 * F, STAGE = 2 * B * 128, CHUNK = 2 * B * 32;
-    constexpr int LOADS = 5;  // a wave's copies in one stage
+    constexpr int F = 2, B = 64 * F, BM = 64 * FM, STAGE = (B + BM) * 128, CHUNK = (B + BM) * 32;
+    constexpr int LOADS = 3 + FM;  // a wave's copies in one stage
     __shared__ __attribute__((aligned(128))) uint8_t lds[4 * STAGE + 3 * CHUNK];
     const int lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int half = wave >> 2, wm = wave >> 1 & 1, wn = wave & 1;
     long long m0;
     int n0, split;
-    tile_place<B>(order, xcd_linear(blockIdx.x, gridDim.x), &m0, &n0, &split);
+    tile_place<BM, B>(order, xcd_linear(blockIdx.x, gridDim.x), &m0, &n0, &split);
     const int first = split * order.split_stages / 2, stages = min(order.split_stages / 2, (p.kb + 7) / 8 - first);
-    const long long rows_x = min(static_cast<long long>(B), p.m - m0), rows_w = min(B, p.n - n0);
+    const long long rows_x = min(static_cast<long long>(BM), p.m - m0), rows_w = min(B, p.n - n0);
     const __amdgpu_buffer_rsrc_t gx = buffer(p.x + m0 * p.pitch, rows_x * p.pitch),
                                  gxs = buffer(p.xs + m0 * p.spitch, rows_x * p.spitch),
                                  gw = buffer(p.w + static_cast<long long>(n0) * p.pitch, rows_w * p.pitch),
@@ -610,34 +613,34 @@ __global__ __launch_bounds__(512, 1) void pair_kernel(MatmulParams p, Tiling ord
         const uint32_t off = s < stages && stage * 8 + copy_block < p.kb ? copy_off + stage * 128 : kOutOfRange;
         const uint32_t to = lds0 + (s & 3) * STAGE + wave * 1024 + i * 8192;
         load_to_lds16(gw, off + i * 64 * p.pitch, to);
-        load_to_lds16(gx, off + i * 64 * p.pitch, to + B * 128);
+        if (i < FM) load_to_lds16(gx, off + i * 64 * p.pitch, to + B * 128);
     };
-    auto copy_scales = [&](int part) {  // quarter part % 4 of chunk part / 4: half the rows of w, or of x
-        const int chunk = part >> 2, rows = (part & 1) * (B / 2);
+    auto copy_scales = [&](int part) {  // quarter part % 4 of chunk part / 4: 64 rows of w, or of x (64 rows in all: twice)
+        const int chunk = part >> 2, of_x = part & 2, rows = of_x && FM == 1 ? 0 : (part & 1) * 64;
         const uint32_t off = (first * 2 + chunk * 8 + copy_word) * 4 < p.spitch ? copy_soff + (first * 2 + chunk * 8) * 4 : kOutOfRange;
-        const uint32_t to = lds0 + 4 * STAGE + chunk % 3 * CHUNK + (part & 2) / 2 * (B * 32) + rows * 32 + wave * 256;
-        load_to_lds4(part & 2 ? gxs : gws, off + rows * p.spitch, to);
+        const uint32_t to = lds0 + 4 * STAGE + chunk % 3 * CHUNK + of_x / 2 * (B * 32) + rows * 32 + wave * 256;
+        load_to_lds4(of_x ? gxs : gws, off + rows * p.spitch, to);
     };
 
-    i32x4 a[2][F], b[2][F];  // operands of two steps in turn
-    int sw[2][F], sx[2][F];  // scale words of a stage, and of the next
+    i32x4 a[2][F], b[2][FM];  // operands of two steps in turn
+    int sw[2][F], sx[2][FM];  // scale words of a stage, and of the next
     const uint8_t* lw = lds + (wn * 32 * F + r) * 128;
-    const uint8_t* lx = lds + (B + wm * 32 * F + r) * 128;
+    const uint8_t* lx = lds + (B + wm * 32 * FM + r) * 128;
     const uint8_t* lws = lds + 4 * STAGE + (wn * 32 * F + r) * 32;
-    const uint8_t* lxs = lds + 4 * STAGE + (B + wm * 32 * F + r) * 32;
+    const uint8_t* lxs = lds + 4 * STAGE + (B + wm * 32 * FM + r) * 32;
     auto read_pair = [&](int s, int j, int f) {
         const int at = (s & 3) * STAGE + ((4 * h + 2 * half + j) ^ ((r >> 1) & 7)) * 16 + f * 4096;
         a[j][f] = *reinterpret_cast<const i32x4*>(lw + at);
-        b[j][f] = *reinterpret_cast<const i32x4*>(lx + at);
+        if (f < FM) b[j][f] = *reinterpret_cast<const i32x4*>(lx + at);
     };
     auto read_scales = [&](int s, int set, int f) {
         const int at = (s >> 2) % 3 * CHUNK + (((s & 3) * 2 + h) ^ (2 * (r >> 3))) * 4 + f * 1024;
         sw[set][f] = *reinterpret_cast<const int*>(lws + at);
-        sx[set][f] = *reinterpret_cast<const int*>(lxs + at);
+        if (f < FM) sx[set][f] = *reinterpret_cast<const int*>(lxs + at);
     };
     float bias[F][16];
     load_bias(p, n0 + wn * 32 * F, bias);  // ahead of the output pass
-    f32x16 acc[F][F] = {};
+    f32x16 acc[FM][F] = {};
 
 #pragma unroll
     for (int q = 0; q < 4; ++q) copy_scales(q);
@@ -660,7 +663,7 @@ __global__ __launch_bounds__(512, 1) void pair_kernel(MatmulParams p, Tiling ord
 #pragma unroll
         for (int f = 0; f < F; ++f) {
             sw[0][f] >>= 16 * half;
-            sx[0][f] >>= 16 * half;
+            if (f < FM) sx[0][f] >>= 16 * half;
         }
 #pragma unroll
         for (int i = 0; i < F; ++i) {
@@ -668,7 +671,7 @@ __global__ __launch_bounds__(512, 1) void pair_kernel(MatmulParams p, Tiling ord
             read_pair(s, 1, i);
             if (i == F - 1) copy_scales(s + 6);
 #pragma unroll
-            for (int f = 0; f < F; ++f) acc[i][f] = mfma<0>(a[0][f], b[0][i], acc[i][f], sw[0][f], sx[0][i]);
+            for (int f = 0; f < (i < FM ? F : 0); ++f) acc[i][f] = mfma<0>(a[0][f], b[0][i], acc[i][f], sw[0][f], sx[0][i]);
             __builtin_amdgcn_sched_barrier(0);
         }
 #pragma unroll
@@ -676,42 +679,43 @@ __global__ __launch_bounds__(512, 1) void pair_kernel(MatmulParams p, Tiling ord
             read_pair(s + 1, 0, i);
             read_scales(s + 1, 1, i);
 #pragma unroll
-            for (int f = 0; f < F; ++f) acc[i][f] = mfma<1>(a[1][f], b[1][i], acc[i][f], sw[0][f], sx[0][i]);
+            for (int f = 0; f < (i < FM ? F : 0); ++f) acc[i][f] = mfma<1>(a[1][f], b[1][i], acc[i][f], sw[0][f], sx[0][i]);
             __builtin_amdgcn_sched_barrier(0);
         }
 #pragma unroll
         for (int f = 0; f < F; ++f) {
             sw[0][f] = sw[1][f];
-            sx[0][f] = sx[1][f];
+            if (f < FM) sx[0][f] = sx[1][f];
         }
     }
     wait_loads<0>();  // the copies past the last stage, which wrote zeros
     barrier();        // and no stage is read any more
 
-    // this group keeps rows 32 half .. + 31 of its waves' 64 and hands the others over
+    // this group keeps rows 32 half .. + 31 of its waves' 64 and hands the others over; of 32 rows group 0 keeps all
     float4* mine = reinterpret_cast<float4*>(lds + wave * 8192) + lane;
     const float4* theirs = reinterpret_cast<const float4*>(lds + (wave ^ 4) * 8192) + lane;
 #pragma unroll
     for (int f = 0; f < F; ++f)
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-            const f32x16& v = half ? acc[0][f] : acc[1][f];
+            const f32x16& v = half ? acc[0][f] : acc[FM - 1][f];
             mine[(f * 4 + g) * 64] = make_float4(v[g * 4], v[g * 4 + 1], v[g * 4 + 2], v[g * 4 + 3]);
         }
     __syncthreads();
+    if (FM == 1 && half) return;
     f32x16 sum[1][F];
 #pragma unroll
     for (int f = 0; f < F; ++f)
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
             const float4 t = theirs[(f * 4 + g) * 64];
-            const f32x16& v = half ? acc[1][f] : acc[0][f];
+            const f32x16& v = half ? acc[FM - 1][f] : acc[0][f];
             sum[0][f][g * 4] = v[g * 4] + t.x + bias[f][g * 4];
             sum[0][f][g * 4 + 1] = v[g * 4 + 1] + t.y + bias[f][g * 4 + 1];
             sum[0][f][g * 4 + 2] = v[g * 4 + 2] + t.z + bias[f][g * 4 + 2];
             sum[0][f][g * 4 + 3] = v[g * 4 + 3] + t.w + bias[f][g * 4 + 3];
         }
-    m0 += wm * 32 * F + half * 32;
+    m0 += wm * 32 * FM + half * 32;
     n0 += wn * 32 * F;
     MatmulParams out = p;
     if constexpr (std::is_same<TY, float>::value) out.y = static_cast<float*>(p.y) + split * p.m * p.ldy;
@@ -755,7 +759,8 @@ bool whole_runs(const MatmulParams& p) {
 template <typename TY>
 void launch_tiles(const MatmulParams& p, bool wide, int splits, int cus, hipStream_t st) {
     const int side = wide ? 256 : 128;
-    const int tiles_m = static_cast<int>((p.m + side - 1) / side), tiles_n = (p.n + side - 1) / side;
+    const bool low = !wide && (p.m + 63) / 64 * ((p.n + 127) / 128) * splits <= cus;  // tiles of 64 rows
+    const int tiles_m = static_cast<int>(low ? (p.m + 63) / 64 : (p.m + side - 1) / side), tiles_n = (p.n + side - 1) / side;
     const int stages = (p.kb + 3) / 4;  // of 128 values; a part has a whole number of chunks of four of 256
     const int split_stages = splits > 1 ? (stages + 8 * splits - 1) / (8 * splits) * 8 : (stages + 1) / 2 * 2;
     const int parts = (stages + split_stages - 1) / split_stages;
@@ -765,8 +770,10 @@ void launch_tiles(const MatmulParams& p, bool wide, int splits, int cus, hipStre
     const bool fast = whole_runs<TY>(p);
     if (wide)
         wide_kernel<TY><<<static_cast<unsigned>(tiles), 256, 0, st>>>(p, order, fast);
+    else if (low)
+        pair_kernel<1, TY><<<static_cast<unsigned>(tiles), 512, 0, st>>>(p, order, fast);
     else if (tiles <= cus)
-        pair_kernel<TY><<<static_cast<unsigned>(tiles), 512, 0, st>>>(p, order, fast);
+        pair_kernel<2, TY><<<static_cast<unsigned>(tiles), 512, 0, st>>>(p, order, fast);
     else
         tile_kernel<TY><<<static_cast<unsigned>(tiles < 2 * cus ? tiles : 2 * cus), 256, 0, st>>>(p, order, fast);
 }
@@ -833,7 +840,7 @@ struct Choice {
 // stages and an output pass; 128-wide tiles share a CU by twos, or have one to
 // themselves (narrow and wide: 8192 x 8192 x 8192 420 and 269 us; x 1024: 76 and
 // 73).  A split sum pays for its parts' traffic and a second launch (128 x 1024 x
-// 16384: 33 us whole, 17 in 8 parts; 500 x 4096 x 4096: 14 and 24 in 2).
+// 16384: 27 us whole, 16 in 8 parts; 500 x 4096 x 4096: 12 and 24 in 2).
 Choice choose(const cfwd_mx_matmul_desc* d, int cus) {
     const double stages = static_cast<double>((mx_blocks(d->k) + 3) / 4);
     const long long t2 = (d->m + 127) / 128 * ((d->n + 127) / 128), t4 = (d->m + 255) / 256 * ((d->n + 255) / 256);
