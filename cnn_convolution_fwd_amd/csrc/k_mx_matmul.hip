@@ -427,9 +427,11 @@ __global__ __launch_bounds__(256, (Resident<S, TY>::kThree ? 3 : 2)) void rows_k
 }
 
 // Wide tiles, for long sums over many tiles: 256 rows of y x 256 columns, one
-// tile a workgroup, one workgroup a CU, 128 x 128 a wave: half the copies of the
-// kernel above for the same products.  (256 accumulators a lane leave no
-// registers in which the next tile's operands could outlast the output pass.)
+// tile a workgroup of eight waves, one workgroup a CU: half the copies of the
+// narrow kernel for the same products.  A wave has 128 x 64 of y, so that every
+// SIMD has two waves to alternate between: four waves of 128 x 128 read a third
+// less from LDS but took longer (8192^3 263 us, 254 so; x 1024 70 and 60; 25088 x
+// 512 x 2048 25 and 21).
 //
 // A stage is 256 values of K here, its rows 128 bytes: a copy costs by the cache
 // line that it touches, whatever it takes of it (from L2 134 GB/s a CU in whole
@@ -438,19 +440,19 @@ __global__ __launch_bounds__(256, (Resident<S, TY>::kThree ? 3 : 2)) void rows_k
 // the last of them all of the stage is in registers, and there the waves meet:
 // the next stage is whole, and the copies of the one after it begin, over the one
 // just read, spread over the matrix instructions of this step and the next
-// (8192^3: 281 us with all of them in one step, 269 so, 231 without copies; 305
-// with four stages of 128 values).
+// (with four waves 281 us with all of them in one step, 269 so, 231 without copies;
+// 305 with four stages of 128 values).
 //
 // Block b of row i lies in slot b ^ ((i >> 1) & 7), scale word q of a row's 8 (four
 // stages', "a chunk") at q ^ (2 ((i >> 3) & 3)): 16 rows' reads of one block
 // then cover the 64 banks (with i & 7, conflicts took 62% of LDS's cycles).
 template <typename TY>
-__global__ __launch_bounds__(256, 1) void wide_kernel(MatmulParams p, Tiling order, bool fast) {
-    constexpr int F = 4, B = 64 * F, STAGE = 2 * B * 128, CHUNK = 2 * B * 32;
+__global__ __launch_bounds__(512, 1) void wide_kernel(MatmulParams p, Tiling order, bool fast) {
+    constexpr int FM = 4, FN = 2, B = 256, STAGE = 2 * B * 128, CHUNK = 2 * B * 32;
     __shared__ __attribute__((aligned(128))) uint8_t lds[2 * STAGE + 2 * CHUNK];
     const int lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wm = wave >> 1, wn = wave & 1;
+    const int wm = wave >> 2, wn = wave & 3;
     long long m0;
     int n0, split;
     tile_place<B, B>(order, xcd_linear(blockIdx.x, gridDim.x), &m0, &n0, &split);
@@ -467,82 +469,82 @@ __global__ __launch_bounds__(256, 1) void wide_kernel(MatmulParams p, Tiling ord
     const int copy_row = wave * 8 + (lane >> 3);
     const int copy_block = (lane & 7) ^ ((copy_row >> 1) & 7), copy_word = (lane & 7) ^ (2 * (wave & 3));
     const uint32_t copy_off = copy_row * p.pitch + copy_block * 16, copy_soff = copy_row * p.spitch + copy_word * 4;
-    auto copy_codes = [&](int stage, int i) {  // i-th of each operand's 8 copies
+    auto copy_codes = [&](int stage, int i) {  // i-th of each operand's 4 copies
         const uint32_t off = stage * 8 + copy_block < p.kb ? copy_off + stage * 128 : kOutOfRange;
-        const uint32_t to = lds0 + (stage & 1) * STAGE + wave * 1024 + i * 4096;
-        load_to_lds16(gw, off + i * 32 * p.pitch, to);
-        load_to_lds16(gx, off + i * 32 * p.pitch, to + B * 128);
+        const uint32_t to = lds0 + (stage & 1) * STAGE + wave * 1024 + i * 8192;
+        load_to_lds16(gw, off + i * 64 * p.pitch, to);
+        load_to_lds16(gx, off + i * 64 * p.pitch, to + B * 128);
     };
-    auto copy_scales = [&](int part, int i) {  // i-th of 4 copies: quarter part % 4 of chunk part / 4, half the rows of w or of x
+    auto copy_scales = [&](int part, int i) {  // i-th of 2 copies: quarter part % 4 of chunk part / 4, half the rows of w or of x
         const int chunk = part >> 2, half = (part & 1) * (B / 2);
         const uint32_t off = chunk * 32 + copy_word * 4 < p.spitch ? copy_soff + chunk * 32 : kOutOfRange;
-        const uint32_t to = lds0 + 2 * STAGE + (chunk & 1) * CHUNK + (part & 2) / 2 * (B * 32) + half * 32 + wave * 256 + i * 1024;
-        load_to_lds4(part & 2 ? gxs : gws, off + (half + i * 32) * p.spitch, to);
+        const uint32_t to = lds0 + 2 * STAGE + (chunk & 1) * CHUNK + (part & 2) / 2 * (B * 32) + half * 32 + wave * 256 + i * 2048;
+        load_to_lds4(part & 2 ? gxs : gws, off + (half + i * 64) * p.spitch, to);
     };
 
-    i32x4 a[2][F], b[2][F];  // operands of two steps in turn
-    int sw[2][F], sx[2][F];  // scale words of a stage, and of the next
-    const uint8_t* lw = lds + (wn * 32 * F + r) * 128;
-    const uint8_t* lx = lds + (B + wm * 32 * F + r) * 128;
-    const uint8_t* lws = lds + 2 * STAGE + (wn * 32 * F + r) * 32;
-    const uint8_t* lxs = lds + 2 * STAGE + (B + wm * 32 * F + r) * 32;
+    i32x4 a[2][FN], b[2][FM];  // operands of two steps in turn
+    int sw[2][FN], sx[2][FM];  // scale words of a stage, and of the next
+    const uint8_t* lw = lds + (wn * 32 * FN + r) * 128;
+    const uint8_t* lx = lds + (B + wm * 32 * FM + r) * 128;
+    const uint8_t* lws = lds + 2 * STAGE + (wn * 32 * FN + r) * 32;
+    const uint8_t* lxs = lds + 2 * STAGE + (B + wm * 32 * FM + r) * 32;
     auto read_pair = [&](int stage, int j, int f) {
         const int at = (stage & 1) * STAGE + ((4 * h + j) ^ ((r >> 1) & 7)) * 16 + f * 4096;
-        a[j & 1][f] = *reinterpret_cast<const i32x4*>(lw + at);
+        if (f < FN) a[j & 1][f] = *reinterpret_cast<const i32x4*>(lw + at);
         b[j & 1][f] = *reinterpret_cast<const i32x4*>(lx + at);
     };
     auto read_scales = [&](int stage, int set, int f) {
         const int at = (stage >> 2 & 1) * CHUNK + (((stage & 3) * 2 + h) ^ (2 * (r >> 3))) * 4 + f * 1024;
-        sw[set][f] = *reinterpret_cast<const int*>(lws + at);
+        if (f < FN) sw[set][f] = *reinterpret_cast<const int*>(lws + at);
         sx[set][f] = *reinterpret_cast<const int*>(lxs + at);
     };
-    f32x16 acc[F][F];
+    f32x16 acc[FM][FN];
     auto multiply = [&](auto j, int i) {
         constexpr int J = decltype(j)::value;
 #pragma unroll
-        for (int f = 0; f < F; ++f) acc[i][f] = mfma<J>(a[J & 1][f], b[J & 1][i], acc[i][f], sw[0][f], sx[0][i]);
+        for (int f = 0; f < FN; ++f) acc[i][f] = mfma<J>(a[J & 1][f], b[J & 1][i], acc[i][f], sw[0][f], sx[0][i]);
         __builtin_amdgcn_sched_barrier(0);
     };
 
 #pragma unroll
-    for (int i = 0; i < 8; ++i) copy_codes(0, i);
+    for (int i = 0; i < 4; ++i) copy_codes(0, i);
 #pragma unroll
     for (int q = 0; q < 5; ++q)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) copy_scales(q, i);
+        for (int i = 0; i < 2; ++i) copy_scales(q, i);
     {  // sums begin with the bias
-        float bias[F][16];
-        load_bias(p, n0 + wn * 32 * F, bias);
+        float bias[FN][16];
+        load_bias(p, n0 + wn * 32 * FN, bias);
 #pragma unroll
-        for (int i = 0; i < F; ++i)
+        for (int i = 0; i < FM; ++i)
 #pragma unroll
-            for (int f = 0; f < F; ++f)
+            for (int f = 0; f < FN; ++f)
 #pragma unroll
                 for (int j = 0; j < 16; ++j) acc[i][f][j] = bias[f][j];
     }
     wait_loads<0>();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) copy_codes(1, i);
+    for (int i = 0; i < 2; ++i) copy_codes(1, i);
     barrier();
 #pragma unroll
-    for (int f = 0; f < F; ++f) {
+    for (int f = 0; f < FM; ++f) {
         read_scales(0, 0, f);
         read_pair(0, 0, f);
     }
     for (int s = 0; s < stages; ++s) {
 #pragma unroll
-        for (int i = 0; i < F; ++i) {
-            copy_codes(s + 1, 4 + i);
+        for (int i = 0; i < FM; ++i) {
+            if (i % 2 == 0) copy_codes(s + 1, 2 + i / 2);
             read_pair(s, 1, i);
             multiply(std::integral_constant<int, 0>{}, i);
         }
 #pragma unroll
-        for (int i = 0; i < F; ++i) {
+        for (int i = 0; i < FM; ++i) {
             read_pair(s, 2, i);
             multiply(std::integral_constant<int, 1>{}, i);
         }
 #pragma unroll
-        for (int i = 0; i < F; ++i) {
+        for (int i = 0; i < FM; ++i) {
             read_pair(s, 3, i);
             multiply(std::integral_constant<int, 2>{}, i);
         }
@@ -550,24 +552,24 @@ __global__ __launch_bounds__(256, 1) void wide_kernel(MatmulParams p, Tiling ord
         wait_loads<0>();
         barrier();
 #pragma unroll
-        for (int i = 0; i < F; ++i) {
-            copy_codes(s + 2, i);
-            copy_scales(s + 5, i);  // a chunk's last quarter two stages before its first stage
+        for (int i = 0; i < FM; ++i) {
+            if (i % 2 == 0) copy_codes(s + 2, i / 2);
+            else copy_scales(s + 5, i / 2);  // a chunk's last quarter two stages before its first stage
             read_pair(s + 1, 0, i);
             read_scales(s + 1, 1, i);
             multiply(std::integral_constant<int, 3>{}, i);
         }
 #pragma unroll
-        for (int f = 0; f < F; ++f) {
-            sw[0][f] = sw[1][f];
+        for (int f = 0; f < FM; ++f) {
+            if (f < FN) sw[0][f] = sw[1][f];
             sx[0][f] = sx[1][f];
         }
     }
     wait_loads<0>();  // the copies past the last stage, which wrote zeros
     barrier();
-    m0 += wm * 32 * F;
-    n0 += wn * 32 * F;
-    write_tile<F, F, TY>(acc, p, m0, n0, fast, lds + wave * (STAGE / 4));
+    m0 += wm * 32 * FM;
+    n0 += wn * 32 * FN;
+    write_tile<FM, FN, TY>(acc, p, m0, n0, fast, lds + wave * (STAGE / 8));
 }
 
 // Few tiles, no more than CUs: 128 columns of y x 128 rows, or x 64 where those
@@ -769,7 +771,7 @@ void launch_tiles(const MatmulParams& p, bool wide, int splits, int cus, hipStre
     const int tiles = tiles_m * tiles_n * parts;
     const bool fast = whole_runs<TY>(p);
     if (wide)
-        wide_kernel<TY><<<static_cast<unsigned>(tiles), 256, 0, st>>>(p, order, fast);
+        wide_kernel<TY><<<static_cast<unsigned>(tiles), 512, 0, st>>>(p, order, fast);
     else if (low)
         pair_kernel<1, TY><<<static_cast<unsigned>(tiles), 512, 0, st>>>(p, order, fast);
     else if (tiles <= cus)
@@ -838,18 +840,18 @@ struct Choice {
 // 53).  Else the cheapest by a model of the time, in us, fitted to measurements
 // over sums of 2 to 128 stages and 8 to 6000 tiles: a round of tiles takes its
 // stages and an output pass; 128-wide tiles share a CU by twos, or have one to
-// themselves (narrow and wide: 8192 x 8192 x 8192 420 and 269 us; x 1024: 76 and
-// 73).  A split sum pays for its parts' traffic and a second launch (128 x 1024 x
+// themselves (narrow and wide: 8192 x 8192 x 8192 420 and 254 us; x 1024: 76 and
+// 60; 2500 x 2900 x 1024: 13 and 15).  A split sum pays for its parts' traffic and a second launch (128 x 1024 x
 // 16384: 27 us whole, 16 in 8 parts; 500 x 4096 x 4096: 12 and 24 in 2).
 Choice choose(const cfwd_mx_matmul_desc* d, int cus) {
     const double stages = static_cast<double>((mx_blocks(d->k) + 3) / 4);
     const long long t2 = (d->m + 127) / 128 * ((d->n + 127) / 128), t4 = (d->m + 255) / 256 * ((d->n + 255) / 256);
     if (stages <= 4 && t2 > cus) return {false, 1, true};
     auto rounds = [](long long tiles, long long slots) { return static_cast<double>((tiles + slots - 1) / slots); };
-    const double alone = 0.22, shared = 0.9, wide = 0.82;  // us for 128 values of K
+    const double alone = 0.22, shared = 0.9, wide = 0.86;  // us for 128 values of K
     double best = t2 <= cus ? stages * alone + 2 : rounds(t2, 2 * cus) * (stages * shared + 3.4);
     Choice c{false, 1};
-    const double four = rounds(t4, cus) * (stages * wide + 11.5);
+    const double four = rounds(t4, cus) * (stages * wide + 8);
     if (four < best) {
         best = four;
         c = {true, 1};
