@@ -80,7 +80,8 @@ __device__ __forceinline__ void store_run(const MatmulParams& p, long long row, 
 //
 // fp32 and bf16 results take a turn through the wave's own LDS area (32 rows, of
 // one or half a set of columns' fragments; 16-byte slots permuted by row instead
-// of padded), so that whole runs of columns are stored.  An MXFP4 block (32
+// of padded, and of bf16 their halves in rows 16 to 31, whose slots are those of
+// rows 0 to 15), so that whole runs of columns are stored.  An MXFP4 block (32
 // columns of a row) is spread over the two lanes r and r + 32, which exchange
 // halves of two blocks, so that each then holds a block's 16 bytes.
 //
@@ -165,8 +166,9 @@ __device__ __forceinline__ void write_tile(const f32x16 (&acc)[FM][FN], const Ma
         uint8_t* y0 = static_cast<uint8_t*>(p.y) + m0 * pitch + static_cast<long long>(n0) * ES;
         const __amdgpu_buffer_rsrc_t y = buffer(y0, (rows - 1) * pitch + (static_cast<long long>(p.ldy) - n0) * ES);
         const uint32_t row0 = lane / SLOTS, slot = lane % SLOTS;
-        auto turned = [](uint32_t row) { return ((SLOTS > 8 ? row : row >> 1) & (SLOTS - 1)) * 16; };
-        const uint32_t put = r * ROW + (turned(r) ^ (ES == 4 ? h * 16 : 0)) + (ES == 4 ? 0 : h * 8);
+        static_assert(SLOTS == 8, "two rows span the banks");
+        auto turned = [](uint32_t row) { return (row >> 1 & 7) * 16; };
+        const uint32_t put = r * ROW + (turned(r) ^ (ES == 4 ? h * 16 : (h ^ r >> 4) * 8));
         auto store_turn = [&](int i, int f0, const u32x4(&t)[RUNS]) {
             const int c = f0 * 32 + static_cast<int>(slot) * RUN, valid = p.n - n0 - c;
             if (fast) {
@@ -223,6 +225,7 @@ __device__ __forceinline__ void write_tile(const f32x16 (&acc)[FM][FN], const Ma
             for (int u = 0; u < RUNS; ++u) {
                 const uint32_t row = u * STEP + row0;
                 t[u] = *reinterpret_cast<const u32x4*>(area + (row * ROW + (turned(row) ^ slot * 16)));
+                if (ES == 2 && u * STEP >= 16) t[u] = u32x4{t[u][2], t[u][3], t[u][0], t[u][1]};
             }
             wave_sync();
         }
