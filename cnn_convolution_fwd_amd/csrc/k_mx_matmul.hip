@@ -33,8 +33,8 @@ __device__ __forceinline__ void barrier() { asm volatile("s_barrier" ::: "memory
 
 struct Tiling {
     int tiles_m, tiles_n;
-    int splits, split_stages;  // parts of the sum over K, each with its own y (m x ldy) behind the last; stages of a part
-    Divisor tiles;             // of one part
+    int split_stages;  // of a part of the sum over K; each part has its own y (m x ldy) behind the last
+    Divisor tiles;     // of one part
     Divisor group, height, last_height;  // of tiles in a group of 8 rows of tiles; of rows in a group, in the last one
 };
 
@@ -766,7 +766,7 @@ void launch_tiles(const MatmulParams& p, bool wide, int splits, int cus, hipStre
     const int stages = (p.kb + 3) / 4;  // of 128 values; a part has a whole number of chunks of four of 256
     const int split_stages = splits > 1 ? (stages + 8 * splits - 1) / (8 * splits) * 8 : (stages + 1) / 2 * 2;
     const int parts = (stages + split_stages - 1) / split_stages;
-    const Tiling order{tiles_m, tiles_n, parts, split_stages, divisor(tiles_m * tiles_n), divisor(8u * tiles_n),
+    const Tiling order{tiles_m, tiles_n, split_stages, divisor(tiles_m * tiles_n), divisor(8u * tiles_n),
                        divisor(8), divisor((tiles_m - 1) % 8 + 1)};
     const int tiles = tiles_m * tiles_n * parts;
     const bool fast = whole_runs<TY>(p);
