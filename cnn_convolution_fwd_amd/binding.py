@@ -930,7 +930,9 @@ def gated_norm(b, residual=None, gate=None, residual_scale: float = 1.0, post: s
         with guard:
             return gated_norm(b, residual, gate, residual_scale, post, post_weight, post_bias, pre, pre_weight,
                               pre_bias, eps, out_dtype, sum_out, out, want_sum)
-    desc = _gated_norm_desc(rows, c, per, residual_scale, eps, post_code, pre_code, b_code, s_code, h_code)
+    # as numbers: a tensor would be kept, and found again, as the object that it is
+    desc = _gated_norm_desc(rows, c, per, float(residual_scale), float(eps), post_code, pre_code, b_code, s_code,
+                            h_code)
     hp, hs = (out.codes.data_ptr(), out.scales.data_ptr()) if h_code == MXFP4 else (_ptr(out), None)
     _check(_lib().cfwd_gated_norm(desc, _ptr(b), _ptr(residual), _ptr(gate), _ptr(post_weight),
                                   _ptr(post_bias), _ptr(pre_weight), _ptr(pre_bias), _ptr(sum_out), hp, hs,
