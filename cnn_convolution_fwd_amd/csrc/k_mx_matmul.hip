@@ -9,19 +9,14 @@ namespace cfwd {
 namespace mx {
 
 // Copies 16 (or 4) bytes a lane from a buffer straight to LDS, lane after lane
-// from `lds` on (wave-uniform); out-of-range lanes write 0.  The compiler does
+// from `lds` on (wave-uniform); out-of-range lanes write 0.  The address in LDS
+// travels in m0, which the compiler itself sets (one wait state before its use).  It does
 // not see these loads: wait_loads() and a barrier come before the data are read.
 __device__ __forceinline__ void load_to_lds16(const __amdgpu_buffer_rsrc_t& b, uint32_t off, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-                 :
-                 : "s"(lds), "v"(off), "s"(b)
-                 : "memory");
+    asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" : : "{m0}"(lds), "v"(off), "s"(b) : "memory");
 }
 __device__ __forceinline__ void load_to_lds4(const __amdgpu_buffer_rsrc_t& b, uint32_t off, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
-                 :
-                 : "s"(lds), "v"(off), "s"(b)
-                 : "memory");
+    asm volatile("s_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" : : "{m0}"(lds), "v"(off), "s"(b) : "memory");
 }
 template <int N>
 __device__ __forceinline__ void wait_loads() {  // until at most N of this wave's loads are outstanding
