@@ -741,7 +741,7 @@ __global__ __launch_bounds__(256) void join_kernel(MatmulParams p, const float* 
         for (int i = 0; i < 8; ++i) v[i] += t[i];
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = activate(v[i], p.act);
+    for (int i = 0; i < 8; ++i) v[i] = activate<TY>(v[i], p.act);
     store_run<TY>(p, row, n, valid, v);
 }
 

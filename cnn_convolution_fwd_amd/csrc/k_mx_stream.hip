@@ -173,7 +173,7 @@ __global__ __launch_bounds__(64 * kWaves) void stream_kernel(MatmulParams p, Div
             for (int i = 0; i < 8; ++i) v[i] += b[i];
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = activate(v[i], p.act);
+        for (int i = 0; i < 8; ++i) v[i] = activate<TY>(v[i], p.act);
         store_run<TY>(p, row, n, valid, v);  // RUNS is a multiple of 4 for MXFP4: a block's quad runs together
     }
 }

@@ -16,6 +16,8 @@
 
 #include "internal.h"
 
+#include <type_traits>
+
 namespace cfwd {
 
 inline long long mx_blocks(long long k) { return (k + 31) / 32; }
@@ -178,12 +180,37 @@ __device__ __forceinline__ uint32_t quantize8(const float (&v)[8], uint32_t* byt
 // Activations in fp32.  NaN stays NaN.  silu(v) = v / (1 + e^-v); gelu is the
 // form with tanh, 0.5 v (1 + tanh z) = v / (1 + e^-2z), z = sqrt(2 / pi) (v +
 // 0.044715 v^3); the powers of 2 are taken directly, with log2(e) in the constants.
+//
+// The argument of a power of 2, rounded once, costs the power a relative error
+// that grows with it: of silu 2.4 units of 2^-24 (rms) for v in [-8, -2], 6 in
+// [-20, -8], 63 at most at -80.  A bf16 or 4-bit result, rounded to 2^-9 or
+// 2^-3, does not show that.  An fp32 silu does, so it takes the argument apart
+// into a whole number and what is left of it, under 1/2 and rounded there (under
+// 6.4 units in all; six more instructions a value, 3 to 12% of a product with many rows).  An fp32 gelu stays as it
+// is: below -2, where the power counts, the form with tanh loses more to 1 + tanh.
+// Both are 0 from where 1 + e^.. passes 2^126 on (silu: v < -87.3, results under 2^-119).
 __device__ __forceinline__ float silu_exponent(float v) { return -1.44269504f * v; }
 __device__ __forceinline__ float gelu_exponent(float v) { return v * (-2.30220820f - 0.10294324f * (v * v)); }
 
+// e^-v = 2^f 2^n.  n stays finite, so that v = inf gives f = -inf and not NaN.
+__device__ __forceinline__ float silu_whole(float v) {
+    return __builtin_amdgcn_fmed3f(__builtin_rintf(silu_exponent(v)), -1024.0f, 1024.0f);
+}
+__device__ __forceinline__ float silu_rest(float v, float n) {
+    return __builtin_fmaf(v, -1.92596299e-8f, __builtin_fmaf(v, -1.44269504f, -n));  // log2(e) in two parts
+}
+
+// TY: float for a result that stays in fp32
+template <typename TY>
 __device__ __forceinline__ float activate(float v, int act) {
     if (act == CFWD_ACT_RELU) return v < 0.0f ? 0.0f : v;
-    if (act == CFWD_ACT_SILU) return v * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(silu_exponent(v)));
+    if (act == CFWD_ACT_SILU) {
+        if constexpr (std::is_same<TY, float>::value) {
+            const float n = silu_whole(v), e = __builtin_amdgcn_exp2f(silu_rest(v, n));
+            return v * __builtin_amdgcn_rcpf(1.0f + __builtin_ldexpf(e, static_cast<int>(n)));
+        }
+        return v * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(silu_exponent(v)));
+    }
     if (act == CFWD_ACT_GELU) return v * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(gelu_exponent(v)));
     return v;
 }
