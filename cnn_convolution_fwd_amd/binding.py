@@ -621,7 +621,8 @@ _MX_CODES = {**{k: v for k, v in _DTYPE_CODES.items() if v != I8}, "mx": MXFP4, 
 
 class MxTensor(NamedTuple):
     """Rows in microscaled 4-bit floating point (format: cfwd.h): ``codes`` uint8 [..., 16 * ceil(cols / 32)],
-    ``scales`` uint8 [..., ceil(cols / 32) rounded up to 4], ``cols`` values a row."""
+    ``scales`` uint8 [..., ceil(cols / 32) rounded up to 4], of which the bytes past the blocks do not count,
+    ``cols`` values a row."""
     codes: object
     scales: object
     cols: int

@@ -175,6 +175,7 @@ __global__ __launch_bounds__(256, 2) void tile_kernel(MatmulParams p, Tiling ord
         read_pair(0, 0, 0, f);
     }
 
+    const int last_bits = scale_bits(p.kb - (stages - 1) * 4 - 2 * h);  // of this half's scales in a row's last stage
     f32x16 acc[F][F] = {};
     int count = 0, group = 0;  // of the stage that is multiplied, among all
     int since = 4;             // stages since the last output pass
@@ -196,10 +197,11 @@ __global__ __launch_bounds__(256, 2) void tile_kernel(MatmulParams p, Tiling ord
                 else wait_loads<CODE_LOADS>();
             }
             barrier();  // all waves' copies for it; and the stage before this one is no longer read
+            const int bits = stage == stages - 1 ? last_bits : 16;
 #pragma unroll
             for (int f = 0; f < F; ++f) {
-                sw[0][f] >>= 16 * h;
-                sx[0][f] >>= 16 * h;
+                sw[0][f] = __builtin_amdgcn_ubfe(sw[0][f], 16 * h, bits);
+                sx[0][f] = __builtin_amdgcn_ubfe(sx[0][f], 16 * h, bits);
             }
 #pragma unroll
             for (int i = 0; i < F; ++i) {
@@ -336,6 +338,7 @@ __global__ __launch_bounds__(256, (Resident<S, TY>::kThree ? 3 : 2)) void rows_k
     const uint8_t* lws = lds + L::kWS + (wn * 32 * F + r) * 4;
     const uint8_t* lxs = lds + XS + (wm * 32 * F + r) * (S * 4);
     const uint8_t* lb = lds + L::kWS + B * 4 + wn * 32 * F * 4 + h * 16;
+    const int last_bits = scale_bits(p.kb - (stages - 1) * 4 - 2 * h);  // of this half's scales in a row's last stage
 
 #pragma unroll
     for (int s = 0; s < R - 1; ++s) {
@@ -367,10 +370,11 @@ __global__ __launch_bounds__(256, (Resident<S, TY>::kThree ? 3 : 2)) void rows_k
             const uint8_t *w = lw + slot * STAGE, *x = lx + stage * STAGE;
             i32x4 a[2][F], b[2][F];
             int sw[F], sx[F];
+            const int bits = stage == stages - 1 ? last_bits : 16;
 #pragma unroll
             for (int f = 0; f < F; ++f) {
-                sw[f] = *reinterpret_cast<const int*>(lws + slot * L::kWords + f * 128) >> 16 * h;
-                sx[f] = *reinterpret_cast<const int*>(lxs + stage * 4 + f * (S * 128)) >> 16 * h;
+                sw[f] = __builtin_amdgcn_ubfe(*reinterpret_cast<const int*>(lws + slot * L::kWords + f * 128), 16 * h, bits);
+                sx[f] = __builtin_amdgcn_ubfe(*reinterpret_cast<const int*>(lxs + stage * 4 + f * (S * 128)), 16 * h, bits);
             }
 #pragma unroll
             for (int j = 0; j < 2; ++j)
@@ -521,10 +525,15 @@ __global__ __launch_bounds__(512, 1) void wide_kernel(MatmulParams p, Tiling ord
 #pragma unroll
     for (int i = 0; i < 2; ++i) copy_codes(1, i);
     barrier();
+    // of this half's scale word in a row's last stage, the bytes of blocks
+    const int last_left = p.kb - (stages - 1) * 8 - 4 * h;
+    const int last_mask = last_left >= 4 ? -1 : (1 << scale_bits(last_left) << scale_bits(last_left - 2)) - 1;
 #pragma unroll
     for (int f = 0; f < FM; ++f) {
         read_scales(0, 0, f);
         read_pair(0, 0, f);
+        if (f < FN) sw[0][f] &= stages == 1 ? last_mask : -1;
+        sx[0][f] &= stages == 1 ? last_mask : -1;
     }
     for (int s = 0; s < stages; ++s) {
 #pragma unroll
@@ -554,10 +563,11 @@ __global__ __launch_bounds__(512, 1) void wide_kernel(MatmulParams p, Tiling ord
             read_scales(s + 1, 1, i);
             multiply(std::integral_constant<int, 3>{}, i);
         }
+        const int mask = s + 2 == stages ? last_mask : -1;
 #pragma unroll
         for (int f = 0; f < FM; ++f) {
-            if (f < FN) sw[0][f] = sw[1][f];
-            sx[0][f] = sx[1][f];
+            if (f < FN) sw[0][f] = sw[1][f] & mask;
+            sx[0][f] = sx[1][f] & mask;
         }
     }
     wait_loads<0>();  // the copies past the last stage, which wrote zeros
@@ -649,6 +659,8 @@ __global__ __launch_bounds__(512, 1) void pair_kernel(MatmulParams p, Tiling ord
     }
     wait_loads<2 * LOADS>();
     barrier();
+    // of this group's and half's scales in a row's last stage, which is in the last part
+    const int row_stages = (p.kb + 7) / 8, last_bits = scale_bits(p.kb - (row_stages - 1) * 8 - 4 * h - 2 * half);
 #pragma unroll
     for (int f = 0; f < F; ++f) {
         read_scales(0, 0, f);
@@ -657,10 +669,11 @@ __global__ __launch_bounds__(512, 1) void pair_kernel(MatmulParams p, Tiling ord
     for (int s = 0; s < stages; ++s) {
         wait_loads<LOADS>();  // this wave's copies for the next stage
         barrier();            // all waves'; and the stage before this one is no longer read
+        const int bits = first + s == row_stages - 1 ? last_bits : 16;
 #pragma unroll
         for (int f = 0; f < F; ++f) {
-            sw[0][f] >>= 16 * half;
-            if (f < FM) sx[0][f] >>= 16 * half;
+            sw[0][f] = __builtin_amdgcn_ubfe(sw[0][f], 16 * half, bits);
+            if (f < FM) sx[0][f] = __builtin_amdgcn_ubfe(sx[0][f], 16 * half, bits);
         }
 #pragma unroll
         for (int i = 0; i < F; ++i) {

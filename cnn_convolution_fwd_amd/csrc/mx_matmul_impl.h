@@ -53,6 +53,10 @@ __device__ __forceinline__ f32x16 mfma(const i32x4& a, const i32x4& b, const f32
     return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a8, b8, c, 4, 4, J, sa, J, sb);
 }
 
+// Bits of the scale bytes of two neighbouring blocks, of which `left` (2 or more: both) are blocks of the row:
+// what the bytes past a row's blocks hold does not count.
+__device__ __forceinline__ int scale_bits(int left) { return min(max(left, 0), 2) * 8; }
+
 // 8 finished values of y's row from column n on, `valid` of them columns of y.
 // An MXFP4 block's four runs belong to a quad of lanes, which all call this.
 template <typename TY>

@@ -385,7 +385,7 @@ cfwd_status cfwd_bottleneck_fwd(const cfwd_bottleneck_desc *desc, const void *x,
  *           even one in the low four bits; bit 3 of a value is its sign, bits
  *           0..2 name 0, 0.5, 1, 1.5, 2, 3, 4, 6 (E2M1).  Values past k are 0.
  *   scales  uint8 [rows][KB rounded up to a multiple of 4]: 2^(byte - 127),
- *           255 = NaN; the bytes past KB are 127.
+ *           255 = NaN; the bytes past KB are written as 127 and do not count when read.
  * Quantisation of a block: with E the biased fp32 exponent of its largest
  * magnitude, byte = max(E - 2, 0), or 255 if the block holds a NaN or an
  * infinity (its codes are then 0); each value / scale is rounded to the
