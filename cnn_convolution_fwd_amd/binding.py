@@ -862,8 +862,8 @@ def gated_norm(b, residual=None, gate=None, residual_scale: float = 1.0, post: s
                sum_out=None, out=None, want_sum: bool = True):
     """(s, h): s = residual_scale * residual + gate * post(b), h = pre(s) over the last axis (cfwd_gated_norm).
 
-    ``b`` (float32 / bfloat16 [..., c], or None) is a block's output,
-    ``residual`` (b's dtype, or float32) the residual stream.  ``gate``
+    ``b`` (float32 / bfloat16 [..., c], or None: its norm counts as 0, so post(b) is
+    ``post_bias``) is a block's output, ``residual`` (b's dtype, or float32) the residual stream.  ``gate``
     [g, c] or [c] has one row for each run of ceil(rows / g) rows (images,
     sequences).  ``post`` and ``pre``: none, rms or layer, with float32 [c]
     weights and biases.  h is in b's dtype, or an MxTensor for ``out_dtype``

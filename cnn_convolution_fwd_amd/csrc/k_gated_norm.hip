@@ -261,7 +261,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void row_kernel(Params p, long l
         }
         request(row + ROWS);
         if (p.post != CFWD_NORM_NONE) {
-            normalise<NV>(f, p.post, valid, p, sum);
+            if (p.a.b) normalise<NV>(f, p.post, valid, p, sum);  // the norm of an absent b is 0, whatever eps is
             if constexpr (NV > 1) post_parameters();
 #pragma unroll
             for (int i = 0; i < NV; ++i)
@@ -381,7 +381,7 @@ __global__ __launch_bounds__(1024) void long_row_kernel(Params p) {
             }
             *rstd = 1.0f / sqrtf(sum(t) * p.inv_c + p.eps);
         };
-        statistics(p.post, get_b, &mean_b, &rstd_b);
+        if (p.a.b) statistics(p.post, get_b, &mean_b, &rstd_b);
         if (p.a.h) statistics(p.pre, get_s, &mean_s, &rstd_s);
         // every lane of a quad walks whole blocks: up to the row's padding in MXFP4
         const int end = MX ? static_cast<int>(p.code_pitch) * 2 : p.c;

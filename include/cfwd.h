@@ -449,8 +449,9 @@ typedef struct {
     cfwd_dtype out_dtype;     /* of h: dtype, or MXFP4 */
 } cfwd_gated_norm_desc;
 
-/* b or residual may be NULL (it then contributes 0), gate NULL (1), s or h
- * NULL (not wanted); weights and biases are fp32 [c] or NULL (1 and 0).
+/* residual may be NULL (it then contributes 0), or b (its norm then counts as 0
+ * whatever eps is, so that post(b) is post_bias), gate NULL (1), s or h NULL
+ * (not wanted); weights and biases are fp32 [c] or NULL (1 and 0).
  * gate: [ceil(rows / rows_per_gate)][c].  h_scales: with an MXFP4 h only.  s
  * may be residual itself, or b itself where both have one type; apart from that no output
  * may overlap an input or the other output.  1 <= c <= 2^22, eps >= 0. */

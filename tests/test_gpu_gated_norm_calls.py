@@ -18,3 +18,19 @@ def test_scalars_given_as_tensors_count_with_their_values_at_the_call():
             got = B.gated_norm(b, r, residual_scale=scale, eps=eps)
             want = B.gated_norm(b, r, residual_scale=value, eps=float(eps))
             assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("c", [7, 64, 1000, 12000, 17000])
+@pytest.mark.parametrize("post", ["rms", "layer"])
+def test_an_absent_block_counts_as_its_posts_bias(c, post):
+    """Also with eps = 0, where the norm of a row of zeros would be 0 / 0."""
+    torch = torch_cuda()
+    r, gate, w, bias = (torch.randn(*s, device="cuda") for s in ((5, c), (c,), (c,), (c,)))
+    for pre in ("rms", "layer", "none"):
+        for more in (dict(), dict(post_weight=w), dict(post_weight=w, post_bias=bias), dict(post_bias=bias, gate=gate)):
+            s, h = B.gated_norm(None, r, residual_scale=0.5, post=post, pre=pre, eps=0.0, **more)
+            add = torch.zeros(c, device="cuda") if "post_bias" not in more else bias * gate if "gate" in more else bias
+            # 0.5 r is exact; the sum, or the sum and the product before it, is rounded to 2^-24
+            assert bool(((s.double() - 0.5 * r.double() - add.double()).abs() <= 2.0 ** -23 * (r.abs() + add.abs())).all())
+            want = B.gated_norm(None, s, pre=pre, eps=0.0)[1]
+            assert (h is None and want is None) or torch.equal(h, want)
