@@ -179,7 +179,8 @@ cfwd_status cfwd_gated_norm(const cfwd_gated_norm_desc* desc, const void* b, con
         for (cfwd_norm_kind kind : {desc->post, desc->pre})
             if (kind < CFWD_NORM_NONE || kind > CFWD_NORM_LAYER) return invalid("unknown norm");
         const size_t es = float_size(desc->dtype), ss = float_size(desc->stream_dtype);
-        if (!es || !ss || ss < es) return invalid("dtype must be fp32 or bf16, stream_dtype fp32 or dtype");
+        if (!es || !ss || (ss < es && (b || gate)))
+            return invalid("dtype must be fp32 or bf16, stream_dtype fp32 or dtype (either without b and gate)");
         const bool h_mx = desc->out_dtype == CFWD_MXFP4;
         if (!h_mx && desc->out_dtype != desc->dtype) return invalid("out_dtype must be dtype or MXFP4");
         if (!(desc->eps >= 0.0f) || std::isinf(desc->eps)) return invalid("eps must be a number >= 0");

@@ -448,15 +448,19 @@ void launch_rows(const Params& p, hipStream_t st) {
     row_kernel<T, NV, TB, TS, MX, TAIL><<<static_cast<unsigned>((p.rows + run - 1) / run), WG, 0, st>>>(p, run);
 }
 
+// A stream narrower than b's type goes with an absent b, and h in that type alone.
+template <typename TB, typename TS>
+constexpr bool kToMx = sizeof(TB) <= sizeof(TS);
+
 template <int T, int NV, typename TB, typename TS>
 void launch_rows(const Params& p, bool to_mx, hipStream_t st) {
-    if (p.c % 8 == 0) {
-        if (to_mx) launch_rows<T, NV, true, false, TB, TS>(p, st);
-        else launch_rows<T, NV, false, false, TB, TS>(p, st);
-    } else {
-        if (to_mx) launch_rows<T, NV, true, true, TB, TS>(p, st);
-        else launch_rows<T, NV, false, true, TB, TS>(p, st);
-    }
+    const bool tail = p.c % 8 != 0;
+    if constexpr (kToMx<TB, TS>)
+        if (to_mx) {
+            tail ? launch_rows<T, NV, true, true, TB, TS>(p, st) : launch_rows<T, NV, true, false, TB, TS>(p, st);
+            return;
+        }
+    tail ? launch_rows<T, NV, false, true, TB, TS>(p, st) : launch_rows<T, NV, false, false, TB, TS>(p, st);
 }
 
 template <typename TB, typename TS>
@@ -465,10 +469,12 @@ void launch(const Params& p, bool to_mx, hipStream_t st) {
     const bool long_row = p.c < 8 || p.c > 16384;  // less than a vector: no place to load its end from
     if (long_row) {
         const unsigned grid = static_cast<unsigned>(std::min<long long>(p.rows, 4096));
-        if (to_mx)
-            long_row_kernel<TB, TS, true><<<grid, 1024, 0, st>>>(p);
-        else
-            long_row_kernel<TB, TS, false><<<grid, 1024, 0, st>>>(p);
+        if constexpr (kToMx<TB, TS>)
+            if (to_mx) {
+                long_row_kernel<TB, TS, true><<<grid, 1024, 0, st>>>(p);
+                return;
+            }
+        long_row_kernel<TB, TS, false><<<grid, 1024, 0, st>>>(p);
     } else if (p.c <= 64) launch_rows<8, 1, TB, TS>(p, to_mx, st);
     else if (p.c <= 128) launch_rows<16, 1, TB, TS>(p, to_mx, st);
     else if (p.c <= 256) launch_rows<32, 1, TB, TS>(p, to_mx, st);
@@ -496,10 +502,10 @@ cfwd_status gated_norm(const cfwd_gated_norm_desc* d, const GatedNormArgs& a, hi
     p.code_pitch = mx_code_pitch(d->c);
     p.a = a;
     const bool to_mx = d->out_dtype == CFWD_MXFP4;
-    if (d->dtype == CFWD_F32)
-        gn::launch<float, float>(p, to_mx, st);
-    else if (d->stream_dtype == CFWD_F32)
-        gn::launch<bf16_t, float>(p, to_mx, st);
+    if (d->stream_dtype == CFWD_F32)
+        d->dtype == CFWD_F32 ? gn::launch<float, float>(p, to_mx, st) : gn::launch<bf16_t, float>(p, to_mx, st);
+    else if (d->dtype == CFWD_F32 && !to_mx)
+        gn::launch<float, bf16_t>(p, false, st);  // no b, no gate: h alone is fp32
     else
         gn::launch<bf16_t, bf16_t>(p, to_mx, st);
     return check_hip(hipGetLastError(), "gated norm launch");

@@ -445,7 +445,7 @@ typedef struct {
     float residual_scale, eps;
     cfwd_norm_kind post, pre;
     cfwd_dtype dtype;         /* of b and gate: fp32 or bf16 */
-    cfwd_dtype stream_dtype;  /* of r and s: fp32, or bf16 where dtype is bf16 */
+    cfwd_dtype stream_dtype;  /* of r and s: fp32, or bf16 where dtype is bf16 or b and gate are NULL */
     cfwd_dtype out_dtype;     /* of h: dtype, or MXFP4 */
 } cfwd_gated_norm_desc;
 

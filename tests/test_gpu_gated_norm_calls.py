@@ -34,3 +34,26 @@ def test_an_absent_block_counts_as_its_posts_bias(c, post):
             assert bool(((s.double() - 0.5 * r.double() - add.double()).abs() <= 2.0 ** -23 * (r.abs() + add.abs())).all())
             want = B.gated_norm(None, s, pre=pre, eps=0.0)[1]
             assert (h is None and want is None) or torch.equal(h, want)
+
+
+@pytest.mark.parametrize("c", [7, 40, 100, 512, 1001, 4096, 8192, 9000, 17000])
+def test_the_norm_of_a_stream_alone_has_either_type(c):
+    """Without b and gate h is float32 or bfloat16 as out_dtype or out says, from a stream of either type."""
+    torch = torch_cuda()
+    full = {"f32": torch.float32, "bf16": torch.bfloat16}
+    r = torch.randn(5, c, device="cuda").bfloat16()
+    for pre in ("rms", "layer"):
+        kw = dict(residual_scale=0.5, pre=pre, pre_weight=torch.randn(c, device="cuda"))
+        for stream in ("f32", "bf16"):
+            _, want = B.gated_norm(None, r.float(), out_dtype="f32", **kw)  # 0.5 r is the same number in all of them
+            for to in ("f32", "bf16"):
+                s, h = B.gated_norm(None, r.to(full[stream]), out_dtype=to, **kw)
+                assert s.dtype == full[stream] and h.dtype == full[to]
+                assert torch.equal(s.float(), 0.5 * r.float()) and torch.equal(h, want.to(full[to]))
+                out = torch.full((5 * c + 64,), 7.0, dtype=full[to], device="cuda")
+                s, h = B.gated_norm(None, r.to(full[stream]), out=out[:5 * c].view(5, c), want_sum=False, **kw)
+                assert s is None and torch.equal(h, want.to(full[to])) and bool((out[5 * c:] == 7).all())
+    with pytest.raises(B.CfwdError):
+        B.gated_norm(r.float(), r)
+    with pytest.raises(B.CfwdError):
+        B.gated_norm(None, r, gate=torch.randn(c, device="cuda"))
