@@ -900,6 +900,8 @@ def gated_norm(b, residual=None, gate=None, residual_scale: float = 1.0, post: s
     post_code, pre_code = _code(_NORMS, post, "norm"), _code(_NORMS, pre, "norm")
     h_code = b_code if out_dtype is None else _code(_MX_CODES, out_dtype, "out_dtype")
     if out is not None:
+        if pre_code == NORM_NONE:
+            raise ValueError("pre none has no h to write to out")
         code = MXFP4 if isinstance(out, MxTensor) else _float_code(out)
         if out_dtype is not None and code != h_code:
             raise ValueError("out is not of out_dtype")

@@ -57,3 +57,13 @@ def test_the_norm_of_a_stream_alone_has_either_type(c):
         B.gated_norm(r.float(), r)
     with pytest.raises(B.CfwdError):
         B.gated_norm(None, r, gate=torch.randn(c, device="cuda"))
+
+
+def test_no_h_for_out():
+    """pre none has no h: an out is refused, not left unwritten."""
+    torch = torch_cuda()
+    r = torch.randn(4, 64, device="cuda")
+    for out in (torch.empty_like(r), B.mx_quantize(r)):
+        with pytest.raises(ValueError):
+            B.gated_norm(r, r, pre="none", out=out)
+    assert B.gated_norm(r, r, pre="none")[1] is None
