@@ -1,6 +1,7 @@
 // C ABI of the 4-bit floating point operators and the gated norms: checks of
 // the arguments, then the launches (k_mx_quant.hip, k_mx_matmul.hip,
 // k_gated_norm.hip).
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <string>
@@ -12,7 +13,8 @@ namespace cfwd {
 namespace {
 
 constexpr int kMaxK = 1 << 22;
-constexpr long long kMaxRows = 1ll << 40;  // keeps every byte count below in 63 bits
+// Both keep the byte counts below in 63 bits: rows of the longest row, and rows at a pitch (in elements).
+constexpr long long kMaxRows = 1ll << 38, kMaxSpan = 1ll << 60;
 
 // No exception leaves the library: what is left to throw is the allocation of an error text.
 template <typename F>
@@ -47,8 +49,14 @@ unsigned long long strided_bytes(long long rows, long long k, long long pitch, s
 }
 
 cfwd_status check_rows(long long rows, int k) {
-    if (rows < 0 || rows > kMaxRows) return invalid("rows must be between 0 and 2^40");
+    if (rows < 0 || rows > kMaxRows) return invalid("rows must be between 0 and 2^38");
     if (k < 1 || k > kMaxK) return invalid("the row length must be between 1 and 2^22");
+    return CFWD_OK;
+}
+
+cfwd_status check_stride(long long rows, int k, long long stride) {
+    if (stride < k || stride > kMaxSpan / std::max(rows, 1ll))
+        return invalid("x_stride must be at least k, and rows times x_stride at most 2^60");
     return CFWD_OK;
 }
 
@@ -60,8 +68,10 @@ cfwd_status check_matmul(const cfwd_mx_matmul_desc* d) {
     if (d->x_dtype != CFWD_MXFP4 && !float_size(d->x_dtype)) return invalid("x must be fp32, bf16 or MXFP4");
     if (d->y_dtype != CFWD_MXFP4 && !float_size(d->y_dtype)) return invalid("y must be fp32, bf16 or MXFP4");
     if (d->act < CFWD_ACT_NONE || d->act > CFWD_ACT_GELU) return invalid("unknown activation");
-    if (d->x_dtype != CFWD_MXFP4 && (d->x_stride < d->k || d->x_stride > kMaxRows))
-        return invalid("x_stride must be at least k");
+    if (d->x_dtype != CFWD_MXFP4) {
+        const cfwd_status st = check_stride(d->m, d->k, d->x_stride);
+        if (st != CFWD_OK) return st;
+    }
     if ((d->m + 31) / 32 * ((d->n + 31) / 32) >= (1ll << 31))
         return set_error(CFWD_ERR_UNSUPPORTED, "y has too many tiles for one launch");
     return CFWD_OK;
@@ -92,7 +102,8 @@ cfwd_status cfwd_mx_quantize(long long rows, int k, cfwd_dtype dtype, const void
         if (s != CFWD_OK) return s;
         const size_t es = float_size(dtype);
         if (!es) return invalid("x must be fp32 or bf16");
-        if (x_stride < k || x_stride > kMaxRows) return invalid("x_stride must be at least k");
+        const cfwd_status st = check_stride(rows, k, x_stride);
+        if (st != CFWD_OK) return st;
         if (rows == 0) return CFWD_OK;
         if (!x || !codes || !scales) return invalid("NULL buffer");
         if (!aligned(x, es) || !aligned(codes, 16) || !aligned(scales, 4))

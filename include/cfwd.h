@@ -393,8 +393,9 @@ cfwd_status cfwd_bottleneck_fwd(const cfwd_bottleneck_desc *desc, const void *x,
  *
  * codes must be 16-byte aligned, scales 4-byte; x and y in fp32 / bf16
  * need only their element's alignment, bias and weights 4 bytes.  rows (m)
- * may be 0: nothing is done.  1 <= k <= 2^22, 1 <= n <= 2^22.  Every call
- * is enqueued on `stream`, allocates nothing and gives the same bits each time. */
+ * may be 0: nothing is done; rows <= 2^38, rows times x_stride <= 2^60,
+ * 1 <= k <= 2^22, 1 <= n <= 2^22.  Every call is enqueued on `stream`,
+ * allocates nothing and gives the same bits each time. */
 
 /* Bytes of the codes and of the scales of `rows` rows of k values. */
 cfwd_status cfwd_mx_size(long long rows, int k, size_t *code_bytes, size_t *scale_bytes);
