@@ -772,8 +772,9 @@ def mx_dequantize(t: MxTensor, dtype="f32", out=None):
 
 
 @functools.lru_cache(maxsize=1024)
-def _mx_matmul_desc(*sizes):
-    """(descriptor reference, workspace bytes) of a product of these sizes; made once, read only."""
+def _mx_matmul_desc(dev, *sizes):
+    """(descriptor reference, workspace bytes) of a product of these sizes on GPU ``dev``, the current one, whose
+    number of CUs decides about the workspace; made once, read only."""
     desc = MxMatmulDesc(*sizes)
     return ctypes.byref(desc), mx_matmul_workspace_size(desc)
 
@@ -843,7 +844,7 @@ def mx_matmul(x, w: MxTensor, bias=None, act: str = "none", out_dtype=None, out=
     if guard is not None:
         with guard:
             return mx_matmul(x, w, bias, act, None, out, workspace)
-    desc, ws_bytes = _mx_matmul_desc(rows, n, k, x_code, y_code, stride, act_code)
+    desc, ws_bytes = _mx_matmul_desc(dev, rows, n, k, x_code, y_code, stride, act_code)
     if workspace is not None:
         ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     elif ws_bytes:

@@ -429,20 +429,23 @@ __global__ __launch_bounds__(1024) void long_row_kernel(Params p) {
     }
 }
 
-// Workgroups of a kernel that the device holds at once (asked for once; 256 CUs where it cannot be).
+// Workgroups of a kernel that the current device holds at once (half of what its CUs' registers could where it cannot be asked).
 template <typename Kernel>
-long long resident(Kernel kernel, int threads) {
-    int dev = 0, cus = 0, per_cu = 0;
-    if (hipGetDevice(&dev) != hipSuccess || hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess ||
-        hipOccupancyMaxActiveBlocksPerMultiprocessor(&per_cu, kernel, threads, 0) != hipSuccess || cus <= 0 || per_cu <= 0)
-        return 256ll * (2048 / threads) / 2;
-    return static_cast<long long>(cus) * per_cu;
+long long resident(PerDevice& known, Kernel kernel, int threads) {
+    return known.get(
+        [&](int) {
+            int per_cu = 0;
+            if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&per_cu, kernel, threads, 0) != hipSuccess) return 0ll;
+            return static_cast<long long>(compute_units()) * per_cu;
+        },
+        256ll * (2048 / threads) / 2);
 }
 
 template <int T, int NV, bool MX, bool TAIL, typename TB, typename TS>
 void launch_rows(const Params& p, hipStream_t st) {
     constexpr int WG = T < 256 ? 256 : T, ROWS = WG / T;
-    static const long long most = resident(row_kernel<T, NV, TB, TS, MX, TAIL>, WG);
+    static PerDevice known;
+    const long long most = resident(known, row_kernel<T, NV, TB, TS, MX, TAIL>, WG);
     const long long groups = (p.rows + ROWS - 1) / ROWS, longest = (1ll << 30) / (p.c * 4ll) / ROWS;
     const long long run = std::min((groups + most - 1) / most, longest) * ROWS;
     row_kernel<T, NV, TB, TS, MX, TAIL><<<static_cast<unsigned>((p.rows + run - 1) / run), WG, 0, st>>>(p, run);

@@ -2,7 +2,6 @@
 #include "mx_matmul_impl.h"
 
 #include <algorithm>
-#include <atomic>
 #include <type_traits>
 
 namespace cfwd {
@@ -820,19 +819,19 @@ void launch_split(const MatmulParams& p, cfwd_dtype y, int splits, int cus, floa
 
 }  // namespace mx
 
+int compute_units() {
+    static PerDevice known;
+    return static_cast<int>(known.get(
+        [](int dev) {
+            int n = 0;
+            return hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) == hipSuccess ? n : 0;
+        },
+        256));
+}
+
 namespace {
 
 size_t round256(size_t v) { return (v + 255) / 256 * 256; }
-
-int compute_units() {  // of the current device; asked for once
-    static std::atomic<int> known[64];
-    int dev = 0, n = 0;
-    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 256;
-    if (int k = known[dev].load(std::memory_order_relaxed)) return k;
-    if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n <= 0) return 256;
-    known[dev].store(n, std::memory_order_relaxed);
-    return n;
-}
 
 // How a product of more rows than the stream kernel takes is cut up: wide
 // tiles or not, and parts of the sum over K.
@@ -922,7 +921,7 @@ cfwd_status mx_matmul(const cfwd_mx_matmul_desc* d, const void* x, const void* x
     p.act = d->act;
     p.y_pitch = static_cast<int>(mx_code_pitch(d->n));
     p.y_spitch = static_cast<int>(mx_scale_pitch(d->n));
-    if (stream) return mx_stream(p, raw ? d->x_dtype : CFWD_MXFP4, d->y_dtype, st);
+    if (stream) return mx_stream(p, raw ? d->x_dtype : CFWD_MXFP4, d->y_dtype, cus, st);
     const bool half = p.kb <= 8;  // of what the rows kernel can hold
     if (c.rows && d->y_dtype == CFWD_F32)
         half ? mx::launch_rows<2, float>(p, cus, st) : mx::launch_rows<4, float>(p, cus, st);

@@ -193,11 +193,11 @@ void launch_stream_y(const MatmulParams& p, cfwd_dtype y, hipStream_t st) {
 }
 
 template <int MT, typename TX>
-void launch_stream_n(const MatmulParams& p, cfwd_dtype y, hipStream_t st) {
+void launch_stream_n(const MatmulParams& p, cfwd_dtype y, int cus, hipStream_t st) {
     // the widest workgroups (fewest readings of x) that still reach every CU
-    if (MT < 4 && p.n >= 256 * 64)  // 64 rows and so many columns go elsewhere
+    if (MT < 4 && p.n >= cus * 64)  // for 64 rows two sets of columns at most
         launch_stream_y<MT, MT < 4 ? 4 : 2, TX>(p, y, st);
-    else if (p.n >= 256 * 32 || y == CFWD_MXFP4)
+    else if (p.n >= cus * 32 || y == CFWD_MXFP4)
         launch_stream_y<MT, 2, TX>(p, y, st);
     else
         launch_stream_y<MT, 1, TX>(p, y, st);
@@ -223,17 +223,17 @@ bool mx_stream_supported(long long m, int n, int k) {
     return m <= 16 || (m <= 32 && nk <= 1 << 26) || (m <= 64 && nk <= 1 << 24 && k <= 8192 && n < 1 << 14);
 }
 
-cfwd_status mx_stream(const mx::MatmulParams& p, cfwd_dtype x, cfwd_dtype y, hipStream_t st) {
+cfwd_status mx_stream(const mx::MatmulParams& p, cfwd_dtype x, cfwd_dtype y, int cus, hipStream_t st) {
     if (x == CFWD_F32)
-        mx::launch_stream_n<1, float>(p, y, st);
+        mx::launch_stream_n<1, float>(p, y, cus, st);
     else if (x == CFWD_BF16)
-        mx::launch_stream_n<1, bf16_t>(p, y, st);
+        mx::launch_stream_n<1, bf16_t>(p, y, cus, st);
     else if (p.m <= 16)
-        mx::launch_stream_n<1, void>(p, y, st);
+        mx::launch_stream_n<1, void>(p, y, cus, st);
     else if (p.m <= 32)
-        mx::launch_stream_n<2, void>(p, y, st);
+        mx::launch_stream_n<2, void>(p, y, cus, st);
     else
-        mx::launch_stream_n<4, void>(p, y, st);
+        mx::launch_stream_n<4, void>(p, y, cus, st);
     return check_hip(hipGetLastError(), "MXFP4 product launch");
 }
 

@@ -16,9 +16,28 @@
 
 #include "internal.h"
 
+#include <atomic>
 #include <type_traits>
 
 namespace cfwd {
+
+// A positive number that belongs to a device, asked for once on each.
+class PerDevice {
+    std::atomic<long long> known_[64] = {};
+
+public:
+    // of the current device; ask() gives it, or 0 where it cannot, and then `otherwise` stands
+    template <typename Ask>
+    long long get(Ask ask, long long otherwise) {
+        int dev = 0;
+        if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return otherwise;
+        long long n = known_[dev].load(std::memory_order_relaxed);
+        if (n == 0 && (n = ask(dev)) > 0) known_[dev].store(n, std::memory_order_relaxed);
+        return n > 0 ? n : otherwise;
+    }
+};
+
+int compute_units();  // of the current device
 
 inline long long mx_blocks(long long k) { return (k + 31) / 32; }
 // bytes of one row: codes (16 for each block), scales (a whole number of words)

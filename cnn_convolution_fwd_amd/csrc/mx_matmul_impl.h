@@ -308,6 +308,6 @@ __device__ __forceinline__ void write_tile(const f32x16 (&acc)[FM][FN], const Ma
 // Few rows (k_mx_stream.hip).  `x`: MXFP4, or x's own type where mx_stream_takes_raw says so.
 bool mx_stream_supported(long long m, int n, int k);
 bool mx_stream_takes_raw(const cfwd_mx_matmul_desc* d);
-cfwd_status mx_stream(const mx::MatmulParams& p, cfwd_dtype x, cfwd_dtype y, hipStream_t st);
+cfwd_status mx_stream(const mx::MatmulParams& p, cfwd_dtype x, cfwd_dtype y, int cus, hipStream_t st);
 
 }  // namespace cfwd

@@ -42,3 +42,15 @@ def test_overlaps_of_the_largest_tensors_are_seen():
     d = ctypes.c_size_t()
     assert B.library().cfwd_mx_size(1 << 38, 1 << 22, ctypes.byref(d), ctypes.byref(ctypes.c_size_t())) == B.OK
     assert d.value == 1 << 59
+
+
+def test_what_depends_on_the_device_is_kept_for_each(monkeypatch):
+    """A workspace depends on the device's CUs: another device's is asked for anew."""
+    asked = iter([100, 200])
+    monkeypatch.setattr(B, "mx_matmul_workspace_size", lambda desc: next(asked))
+    B._mx_matmul_desc.cache_clear()
+    try:
+        sizes = (70, 8, 64, B.BF16, B.F32, 64, 0)
+        assert [B._mx_matmul_desc(dev, *sizes)[1] for dev in (0, 1, 0, 1)] == [100, 200, 100, 200]
+    finally:
+        B._mx_matmul_desc.cache_clear()
