@@ -10,8 +10,9 @@
 // and codes of 0, so that the whole block, and every product with it, is NaN.
 // A scaled value becomes the nearest of 0, 0.5, 1, 1.5, 2, 3, 4, 6 (a tie to
 // the even code), its sign kept (code bit 3).  gfx950's conversion instruction
-// does exactly that (compared with the bit-level rule on all bf16 values, all
-// ties and 2^20 random values).
+// does exactly that: the tests hold it to the definition, bit for bit, over every
+// bf16 value up to six binades below its block's largest, fp32 ties and their
+// neighbours, and 2^20 random fp32 values.
 #pragma once
 
 #include "internal.h"
