@@ -10,14 +10,16 @@
 // and a thread holds NV vectors of 8 values.  A workgroup walks a run of rows:
 // weights and gate, which would otherwise cost as many bytes of L2 as the row
 // of HBM, stay in registers, and a row's values are requested while the row
-// before it is worked on.  That lasts only if no memory access is behind a
+// before it is worked on.  That lasts only if a row's accesses are not behind a
 // branch (a wait then has to cover the path with the fewest accesses after it),
 // so absent tensors, rows past the end and columns past the row are accesses out
-// of a buffer's range, which load zeros and store nothing.  All statistics are fp32; the variance is summed from
-// the centred values.  s and h are rounded once, h from the unrounded s.  Rows
-// too long for registers run in a second kernel that reads them again for each
-// sum.  16384 x 8192 in bf16 with both norms: 206 us, 5.2 TB/s (a plain copy's
-// rate); 25088 x 512 to MXFP4: 17.6; one row of 4096: 3.6.
+// of a buffer's range, which load zeros and store nothing.  Two loads are behind
+// one: the gate's next row, once for each run of rows that shares it, and the
+// weights of rows over 8192, which find no registers and are read for each row.
+// All statistics are fp32; the variance is summed from the centred values.  s and
+// h are rounded once, h from the unrounded s.  16384 x 8192 in bf16 with both
+// norms: 200 to 217 us, 4.9 to 5.4 TB/s (a plain copy: 5.4); 25088 x 512 to MXFP4:
+// 16.5; one row of 4096: 3.6.
 #include "gated_norm.h"
 #include "mx.h"
 
@@ -312,8 +314,11 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void row_kernel(Params p, long l
     }
 }
 
-// Rows of any length: 1024 threads walk the row once for each sum and once
-// for the outputs.  s is formed anew in each walk, from b and r alone, so s
+// Rows too long for registers, and those of less than a vector: 1024 threads walk
+// the row once for each sum and once for the outputs.  Both norms RMS in bf16: 4096
+// x 20000 235 us (121 for its bytes read once; b is read three times and r twice,
+// which is 212), 4096 x 65536 to MXFP4 660 (324; 621), one row of 20000 8.5.  Rows
+// under 8 values leave nearly all threads without work: 18 ns a row, 100352 x 4 1850 us.  s is formed anew in each walk, from b and r alone, so s
 // may be written over either (the last walk reads a value before it writes it).
 template <typename TB, typename TS, bool MX>
 __global__ __launch_bounds__(1024) void long_row_kernel(Params p) {

@@ -259,7 +259,7 @@ __global__ __launch_bounds__(256, 2) void tile_kernel(MatmulParams p, Tiling ord
 // barrier, and begins sums with the bias, which travels to LDS with w's scale
 // words (both by waves' own fourth of one copy).
 //
-// 100352 x 1024 x 256, gelu, bf16: 63 us (narrow tiles 76); x in MXFP4 to y in
+// 100352 x 1024 x 256, gelu, bf16: 57 us (narrow tiles 76); x in MXFP4 to y in
 // MXFP4, 25088 x 2048 x 512, gelu: 41 (47), without gelu 30 (37).  Quantising x
 // on its way to LDS was slower than a launch of its own before (80 us
 // against 73 with it, 53 against 46), because every workgroup then waits for memory.
@@ -583,8 +583,11 @@ __global__ __launch_bounds__(512, 1) void wide_kernel(MatmulParams p, Tiling ord
 // between, and the groups' sums meet in LDS at the end, each group finishing
 // half of each wave's rows (2048 x 2048 x 8192: 26 us, 34 with the narrow kernel;
 // 500 x 4096 x 4096 by 64 rows 12.0, by 128 13.5, narrow 17.6).  A fifth stage in
-// LDS gained nothing: memory's latency is not what bounds it, but a CU's rate
-// of copies to LDS and the chain from a stage's barrier to the next.
+// LDS gained nothing: memory's latency is not what bounds it.  Nor are the two
+// rates: of a stage's 0.45 us (64 rows) its products need 0.17 and its copies 0.24
+// (24.5 KB of codes and 64 lines of scales at 134 GB/s a CU).  It is the chain
+// from a stage's barrier over LDS reads, matrix instructions and the wait to the
+// next, with two waves a SIMD to hide it.
 //
 // A stage is 256 values of K (whole cache lines, rows and slots as in the wide
 // kernel); LDS holds four, used as by the narrow kernel: s is multiplied, s + 1

@@ -3,7 +3,7 @@
 // Both directions are one pass: a thread owns 8 consecutive values of a row
 // (16 bytes of bf16), four adjacent lanes a block of 32, whose largest
 // magnitude they find with two cross-lane moves.  Bound by HBM traffic (100352 x
-// 256 in bf16, 64 MB: 11.4 to 13 us one way, 10 to 11.7 back, 5 to 6 TB/s with part of
+// 256 in bf16, 64 MB: 11.3 to 13.1 us one way, 11.2 to 11.7 back, 5 to 6 TB/s with part of
 // it from the last-level cache); at small sizes by the launch (1.7 us).
 #include "mx.h"
 
