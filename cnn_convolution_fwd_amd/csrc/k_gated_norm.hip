@@ -315,11 +315,12 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void row_kernel(Params p, long l
 }
 
 // Rows too long for registers, and those of less than a vector: 1024 threads walk
-// the row once for each sum and once for the outputs.  Both norms RMS in bf16: 4096
-// x 20000 235 us (121 for its bytes read once; b is read three times and r twice,
-// which is 212), 4096 x 65536 to MXFP4 660 (324; 621), one row of 20000 8.5.  Rows
-// under 8 values leave nearly all threads without work: 18 ns a row, 100352 x 4 1850 us.  s is formed anew in each walk, from b and r alone, so s
-// may be written over either (the last walk reads a value before it writes it).
+// the row once for each sum and once for the outputs.  s is formed anew in each
+// walk, from b and r alone, so s may be written over either (the last walk reads a
+// value before it writes it).  Both norms RMS in bf16: 4096 x 20000 235 us (121 for
+// its bytes read once; b is read three times and r twice, which is 212), 4096 x
+// 65536 to MXFP4 660 (324; 621), one row of 20000 8.5.  Rows under 8 values leave
+// nearly all threads without work: 18 ns a row, 100352 x 4 1850 us.
 template <typename TB, typename TS, bool MX>
 __global__ __launch_bounds__(1024) void long_row_kernel(Params p) {
     __shared__ float slots[32];
