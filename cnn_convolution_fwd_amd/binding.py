@@ -37,6 +37,9 @@ EXPORTED = [
     "cfwd_convert_layout", "cfwd_unpack_int4",
     "cfwd_mx_size", "cfwd_mx_quantize", "cfwd_mx_dequantize", "cfwd_mx_matmul_workspace_size", "cfwd_mx_matmul",
     "cfwd_gated_norm",
+    "cfwd_rope_turns", "cfwd_rope", "cfwd_mx_cache_write", "cfwd_mx_cache_read",
+    "cfwd_mx_cache_attention_workspace_size", "cfwd_mx_cache_attention", "cfwd_attention_workspace_size",
+    "cfwd_attention",
 ]
 ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU = 0, 1, 2, 3
 NORM_NONE, NORM_RMS, NORM_LAYER = 0, 1, 2
@@ -80,6 +83,50 @@ class GatedNormDesc(ctypes.Structure):
                 ("out_dtype", ctypes.c_int)]
 
 
+class RopeDesc(ctypes.Structure):
+    """cfwd_rope_desc: rotary positions of q and k [tokens, heads, dim]."""
+    _fields_ = [("tokens", ctypes.c_longlong)] + \
+               [(n, ctypes.c_int) for n in ("q_heads", "k_heads", "head_dim", "pairs", "axes", "adjacent",
+                                            "wide_positions", "dtype")] + \
+               [(n, ctypes.c_longlong) for n in ("q_stride", "q_head_stride", "k_stride", "k_head_stride",
+                                                 "q_out_stride", "q_out_head_stride", "k_out_stride",
+                                                 "k_out_head_stride")]
+
+
+class MxCacheParts(ctypes.Structure):
+    """cfwd_mx_cache: the paged cache's sizes and the addresses of its four parts."""
+    _fields_ = [(n, ctypes.c_int) for n in ("pages", "page_size", "kv_heads", "head_dim")] + \
+               [(n, ctypes.c_void_p) for n in ("k_codes", "k_scales", "v_codes", "v_scales")]
+
+
+class MxCacheWriteDesc(ctypes.Structure):
+    """cfwd_mx_cache_write_desc."""
+    _fields_ = [("tokens", ctypes.c_longlong), ("dtype", ctypes.c_int), ("wide_slots", ctypes.c_int)] + \
+               [(n, ctypes.c_longlong) for n in ("k_stride", "k_head_stride", "v_stride", "v_head_stride")]
+
+
+class MxCacheReadDesc(ctypes.Structure):
+    """cfwd_mx_cache_read_desc."""
+    _fields_ = [("tokens", ctypes.c_longlong), ("sequences", ctypes.c_int), ("table_pitch", ctypes.c_int),
+                ("dtype", ctypes.c_int)]
+
+
+class MxCacheAttentionDesc(ctypes.Structure):
+    """cfwd_mx_cache_attention_desc."""
+    _fields_ = [(n, ctypes.c_int) for n in ("sequences", "tokens", "q_heads", "table_pitch")] + \
+               [("scale", ctypes.c_float), ("dtype", ctypes.c_int)] + \
+               [(n, ctypes.c_longlong) for n in ("q_seq_stride", "q_stride", "q_head_stride")]
+
+
+class AttentionDesc(ctypes.Structure):
+    """cfwd_attention_desc: packed prompts."""
+    _fields_ = [("q_tokens", ctypes.c_longlong), ("k_tokens", ctypes.c_longlong)] + \
+               [(n, ctypes.c_int) for n in ("sequences", "q_heads", "kv_heads", "head_dim", "causal")] + \
+               [("scale", ctypes.c_float), ("dtype", ctypes.c_int)] + \
+               [(n, ctypes.c_longlong) for n in ("q_stride", "q_head_stride", "k_stride", "k_head_stride", "v_stride",
+                                                 "v_head_stride")]
+
+
 class Algo(ctypes.Structure):
     _fields_ = [("kind", ctypes.c_int), ("config_id", ctypes.c_int), ("median_ms", ctypes.c_float)]
 
@@ -114,6 +161,8 @@ def _lib():
         lib.cfwd_last_error.restype = ctypes.c_char_p
         lib.cfwd_algo_name.restype = ctypes.c_char_p
         lib.cfwd_algo_name.argtypes = [Algo]
+        lib.cfwd_rope_turns.restype = ctypes.c_uint64
+        lib.cfwd_rope_turns.argtypes = [ctypes.c_double]
         sigs = {
             "cfwd_output_dims": [dp, P(ctypes.c_int), P(ctypes.c_int)],
             "cfwd_resolve_algo": [dp, Algo, P(Algo)],
@@ -145,6 +194,13 @@ def _lib():
             "cfwd_mx_matmul_workspace_size": [P(MxMatmulDesc), P(sz)],
             "cfwd_mx_matmul": [P(MxMatmulDesc)] + [vp] * 8 + [sz, vp],
             "cfwd_gated_norm": [P(GatedNormDesc)] + [vp] * 11,
+            "cfwd_rope": [P(RopeDesc)] + [vp] * 7,
+            "cfwd_mx_cache_write": [P(MxCacheWriteDesc), P(MxCacheParts)] + [vp] * 4,
+            "cfwd_mx_cache_read": [P(MxCacheReadDesc), P(MxCacheParts)] + [vp] * 5,
+            "cfwd_mx_cache_attention_workspace_size": [P(MxCacheAttentionDesc), P(MxCacheParts), P(sz)],
+            "cfwd_mx_cache_attention": [P(MxCacheAttentionDesc), P(MxCacheParts)] + [vp] * 5 + [sz, vp],
+            "cfwd_attention_workspace_size": [P(AttentionDesc), P(sz)],
+            "cfwd_attention": [P(AttentionDesc)] + [vp] * 7 + [sz, vp],
             "cfwd_fastrun_choose": [P(Algo), P(ctypes.c_float), ctypes.c_int, ctypes.c_int, P(ctypes.c_int),
                                     P(ctypes.c_int)],
         }
@@ -942,3 +998,377 @@ def gated_norm(b, residual=None, gate=None, residual_scale: float = 1.0, post: s
                                   _ptr(post_bias), _ptr(pre_weight), _ptr(pre_bias), _ptr(sum_out), hp, hs,
                                   _stream_of(dev)))
     return sum_out, out
+
+
+# ------------------------------------------------------- rotary positions, the MXFP4 cache and attention
+
+class RopeTable(NamedTuple):
+    """Rotary positions' axes and frequencies (``rope_table``): ``pairs`` int64 [pairs, 2] on the GPU, ``axes``."""
+    pairs: object
+    axes: int
+
+
+_ROPE_ORDERS = ("runs", "turns", "each")
+
+
+def rope_table(rotary_dim: int, sections: Optional[Sequence[int]] = None, base: float = 10000.0, order: str = "runs",
+               frequencies: Optional[Sequence[float]] = None, device="cuda") -> RopeTable:
+    """Axis and frequency of each of ``rotary_dim / 2`` pairs, for ``rope``; made once.
+
+    ``sections``: pairs of each axis (time, height, width, ...), rotary_dim / 2
+    in all; default one axis.  ``order`` "runs": the first section's pairs belong
+    to axis 0, the next ones to axis 1, ..., and the frequencies
+    base^(-2 i / rotary_dim) run on over all pairs i; "turns": the axes take
+    turns pair by pair until their sections are used up, with the same
+    frequencies; "each": as "runs", but every axis has frequencies of its own,
+    base^(-i / n) for its n pairs.  ``frequencies`` (radians a position, one for
+    each pair) take the place of these powers of ``base``.
+    """
+    torch = _torch()
+    if rotary_dim < 0 or rotary_dim % 2:
+        raise ValueError("rotary_dim must be even")
+    pairs = rotary_dim // 2
+    sections = [pairs] if sections is None else [int(n) for n in sections]
+    if not sections or min(sections) < 0 or sum(sections) != pairs:
+        raise ValueError("sections must be %d pairs in all" % pairs)
+    if order not in _ROPE_ORDERS:
+        raise ValueError("unknown order %r (one of %s)" % (order, ", ".join(_ROPE_ORDERS)))
+    if order == "turns":
+        rounds = range(max(sections))
+        axes = [a for i in rounds for a, n in enumerate(sections) if i < n]
+    else:
+        axes = [a for a, n in enumerate(sections) for _ in range(n)]
+    if frequencies is not None:
+        freq = [float(f) for f in frequencies]
+        if len(freq) != pairs:
+            raise ValueError("frequencies must be %d numbers" % pairs)
+    elif order == "each":
+        freq = [float(base) ** (-i / n) for n in sections for i in range(n)]
+    else:
+        freq = [float(base) ** (-i / pairs) for i in range(pairs)]
+    turns = [_lib().cfwd_rope_turns(f) for f in freq]
+    signed = [t - (1 << 64) if t >> 63 else t for t in turns]
+    table = torch.tensor([[t, a] for t, a in zip(signed, axes)], dtype=torch.int64).reshape(pairs, 2)
+    return RopeTable(table.to(device), len(sections))
+
+
+def _int_code(t, what: str) -> int:
+    """0 for an int32 tensor, 1 for int64."""
+    torch = _torch()
+    if t.dtype == torch.int32:
+        return 0
+    if t.dtype == torch.int64:
+        return 1
+    raise TypeError("%s must be int32 or int64" % what)
+
+
+def _int32(dev: int, t, shape, what: str):
+    if t.dtype != _torch().int32 or t.shape != shape:
+        raise ValueError("%s must be int32 %s" % (what, list(shape)))
+    _check_on(dev, t)
+
+
+def _heads_of(t, what: str) -> Tuple[int, int, int, int, int]:
+    """(tokens, heads, dim, token stride, head stride) of [tokens, heads, dim] with dense dims; the stride of an axis of
+    one, which may be any number, as in a dense tensor."""
+    shape = t.shape
+    if len(shape) != 3:
+        raise ValueError("%s must be [tokens, heads, dim]" % what)
+    st, sh, sd = t.stride()
+    if sd != 1 and shape[2] > 1:
+        raise ValueError("the last axis of %s must be dense" % what)
+    tokens, heads, dim = shape
+    return tokens, heads, dim, st if tokens > 1 else heads * dim, sh if heads > 1 else dim
+
+
+@functools.lru_cache(maxsize=1024)
+def _rope_desc(*sizes):
+    return ctypes.byref(RopeDesc(*sizes))
+
+
+def rope(q, k, positions, table: RopeTable, adjacent: bool = False, q_out=None, k_out=None):
+    """(q, k) turned by their positions (cfwd_rope).
+
+    ``q`` [tokens, heads, dim] and ``k`` (the same with its own number of heads,
+    or None) are float32 or bfloat16 with dense dims; tokens and heads may be
+    strided, as parts of one projection's output are.  ``positions``: int32 or
+    int64 [tokens, axes] (or [tokens] for one axis).  ``adjacent``: pairs are values
+    2 i and 2 i + 1 of a head instead of i and i + rotary_dim / 2.  ``q_out`` and
+    ``k_out`` may be ``q`` and ``k`` themselves.
+    """
+    torch = _torch()
+    dev = q.get_device()
+    tokens, heads, dim, qs, qh = _heads_of(q, "q")
+    code = _float_code(q)
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    elif q_out.shape != q.shape or q_out.dtype != q.dtype or q_out.get_device() != dev:
+        raise ValueError("q_out must be as q")
+    _, _, _, qos, qoh = _heads_of(q_out, "q_out")
+    kh = ks = khs = kos = koh = 0
+    if k is not None:
+        kt, kh, kd, ks, khs = _heads_of(k, "k")
+        if kt != tokens or kd != dim or k.dtype != q.dtype or k.get_device() != dev:
+            raise ValueError("k must have q's tokens, dim, dtype and device")
+        if k_out is None:
+            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        elif k_out.shape != k.shape or k_out.dtype != k.dtype or k_out.get_device() != dev:
+            raise ValueError("k_out must be as k")
+        _, _, _, kos, koh = _heads_of(k_out, "k_out")
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    pairs, axes = table
+    if positions.shape != (tokens, axes) and not (axes == 1 and positions.shape == (tokens,)):
+        raise ValueError("positions must be [%d, %d]" % (tokens, axes))
+    wide = _int_code(positions, "positions")
+    if pairs.dtype != torch.int64 or pairs.dim() != 2 or pairs.shape[1] != 2:
+        raise ValueError("table must come from rope_table")
+    _check_on(dev, positions, pairs)
+    guard = _guard(dev)
+    if guard is not None:
+        with guard:
+            return rope(q, k, positions, table, adjacent, q_out, k_out)
+    desc = _rope_desc(tokens, heads, kh, dim, pairs.shape[0], axes, int(bool(adjacent)), wide, code, qs, qh, ks, khs,
+                      qos, qoh, kos, koh)
+    _check(_lib().cfwd_rope(desc, q.data_ptr(), _ptr(k), positions.data_ptr(), pairs.data_ptr(), q_out.data_ptr(),
+                            _ptr(k_out), _stream_of(dev)))
+    return q_out, k_out
+
+
+class MxCache(NamedTuple):
+    """A paged cache of keys and values: ``k`` and ``v`` are MxTensors [pages, heads, page_size, dim].  Token t of a
+    sequence is row t % page_size of the page that its page table names at t // page_size."""
+    k: MxTensor
+    v: MxTensor
+
+
+def mx_cache(pages: int, page_size: int, heads: int, dim: int, device="cuda") -> MxCache:
+    """An MxCache whose values are all 0."""
+    torch = _torch()
+    cp, sp = mx_pitches(dim)
+    zeros = lambda pitch: torch.zeros(pages, heads, page_size, pitch, dtype=torch.uint8, device=device)  # noqa: E731
+    return MxCache(MxTensor(zeros(cp), zeros(sp), dim), MxTensor(zeros(cp), zeros(sp), dim))
+
+
+def _check_cache(cache: MxCache):
+    """(GPU, sizes (pages, page_size, heads, dim), addresses) of a cache whose parts fit each other."""
+    if not isinstance(cache, MxCache):
+        raise TypeError("cache must be an MxCache")
+    (kc, ks, dim), (vc, vs, v_dim) = cache
+    shape, u8 = kc.shape, _torch().uint8
+    cp, sp = mx_pitches(dim)
+    lead = shape[:-1]
+    if len(shape) != 4 or v_dim != dim or vc.shape != shape or shape[3] != cp or not cp or ks.shape != (*lead, sp) \
+            or vs.shape != ks.shape:
+        raise ValueError("the cache's parts must be MxTensors [pages, heads, page_size, dim] of one shape")
+    if kc.dtype != u8 or ks.dtype != u8 or vc.dtype != u8 or vs.dtype != u8:
+        raise TypeError("codes and scales must be uint8")
+    dev = kc.get_device()
+    _check_on(dev, kc, ks, vc, vs)
+    return dev, (lead[0], lead[2], lead[1], dim), (kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr())
+
+
+@functools.lru_cache(maxsize=1024)
+def _mx_cache_write_desc(*sizes):
+    return ctypes.byref(MxCacheWriteDesc(*sizes))
+
+
+def mx_cache_write(k, v, cache: MxCache, slots):
+    """Quantises ``k`` and ``v`` [tokens, heads, dim] into the cache (cfwd_mx_cache_write).
+
+    float32 or bfloat16 with dense dims, tokens and heads may be strided.
+    ``slots`` (int32 or int64 [tokens]): page * page_size + offset of each token; one
+    that is negative, or past the cache, leaves its token out.  Slots must differ from each other.
+    """
+    dev, sizes, parts = _check_cache(cache)
+    tokens, heads, dim, ks, kh = _heads_of(k, "k")
+    vt, vheads, vd, vs, vh = _heads_of(v, "v")
+    if (heads, dim) != sizes[2:] or (vt, vheads, vd) != (tokens, heads, dim) or v.dtype != k.dtype:
+        raise ValueError("k and v must be [tokens, %d, %d] of one dtype" % sizes[2:])
+    if k.get_device() != dev or v.get_device() != dev:
+        raise ValueError("tensors must be on one GPU")
+    code, wide = _float_code(k), _int_code(slots, "slots")
+    if slots.shape != (tokens,):
+        raise ValueError("slots must be [%d]" % tokens)
+    _check_on(dev, slots)
+    guard = _guard(dev)
+    if guard is not None:
+        with guard:
+            return mx_cache_write(k, v, cache, slots)
+    _check(_lib().cfwd_mx_cache_write(_mx_cache_write_desc(tokens, code, wide, ks, kh, vs, vh),
+                                      ctypes.byref(MxCacheParts(*sizes, *parts)), k.data_ptr(), v.data_ptr(),
+                                      slots.data_ptr(), _stream_of(dev)))
+
+
+@functools.lru_cache(maxsize=1024)
+def _mx_cache_read_desc(*sizes):
+    return ctypes.byref(MxCacheReadDesc(*sizes))
+
+
+def _check_table(dev: int, table) -> Tuple[int, int]:
+    if table.dtype != _torch().int32 or table.dim() != 2:
+        raise ValueError("page_table must be int32 [sequences, pages]")
+    _check_on(dev, table)
+    return table.shape
+
+
+def mx_cache_read(cache: MxCache, page_table, starts, tokens: int, dtype="bf16", k_out=None, v_out=None):
+    """(k, v) [tokens, heads, dim]: the first tokens of every sequence, packed, in float32 or bfloat16, both exact
+    (cfwd_mx_cache_read).
+
+    ``page_table`` int32 [sequences, pages]; ``starts`` int32 [sequences + 1]: row starts[i] of the outputs is
+    sequence i's token 0.  Rows behind starts[-1] are left as they were (undefined where the call allocates them).
+    """
+    torch = _torch()
+    dev, sizes, parts = _check_cache(cache)
+    sequences, pitch = _check_table(dev, page_table)
+    _int32(dev, starts, (sequences + 1,), "starts")
+    shape = (int(tokens), sizes[2], sizes[3])
+    outs = []
+    for out in (k_out, v_out):
+        if out is None:
+            code = _code(_MX_CODES, dtype, "dtype")
+            if code == MXFP4:
+                raise ValueError("dtype must be f32 or bf16")
+            out = torch.empty(shape, dtype=torch.float32 if code == F32 else torch.bfloat16, device=cache.k.codes.device)
+        else:
+            if tuple(out.shape) != shape:
+                raise ValueError("outputs must have the shape %s" % (shape,))
+            _check_on(dev, out)
+        outs.append(out)
+    code = _float_code(outs[0])
+    if outs[1].dtype != outs[0].dtype:
+        raise ValueError("both outputs must have one dtype")
+    guard = _guard(dev)
+    if guard is not None:
+        with guard:
+            return mx_cache_read(cache, page_table, starts, tokens, dtype, *outs)
+    _check(_lib().cfwd_mx_cache_read(_mx_cache_read_desc(shape[0], sequences, pitch, code),
+                                     ctypes.byref(MxCacheParts(*sizes, *parts)), page_table.data_ptr(),
+                                     starts.data_ptr(), outs[0].data_ptr(), outs[1].data_ptr(), _stream_of(dev)))
+    return outs[0], outs[1]
+
+
+def _workspace(workspace, need: int, device, dev: int):
+    """(tensor, address, bytes) of the caller's workspace, or of a new one where one is needed."""
+    if workspace is not None:
+        _check_on(dev, workspace)
+        return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    if not need:
+        return None, None, 0
+    workspace = _torch().empty(need, dtype=_torch().uint8, device=device)
+    return workspace, workspace.data_ptr(), need
+
+
+@functools.lru_cache(maxsize=1024)
+def _mx_cache_attention_desc(dev, cache_sizes, *sizes):
+    """(descriptor reference, workspace bytes) on GPU ``dev``, the current one, whose CUs decide about the workspace."""
+    desc, b = MxCacheAttentionDesc(*sizes), ctypes.c_size_t()
+    _check(_lib().cfwd_mx_cache_attention_workspace_size(ctypes.byref(desc), ctypes.byref(MxCacheParts(*cache_sizes)),
+                                                         ctypes.byref(b)))
+    return ctypes.byref(desc), b.value
+
+
+def mx_cache_attention(q, cache: MxCache, page_table, lengths, scale: Optional[float] = None, out=None, workspace=None):
+    """softmax(scale q K^T) V over each sequence's cache (cfwd_mx_cache_attention).
+
+    ``q`` bfloat16 [sequences, heads, dim], or [sequences, tokens, heads, dim]
+    for several new tokens each: query i of them sees the first lengths - tokens + 1 + i
+    tokens of its sequence.  ``page_table`` int32 [sequences, pages], ``lengths`` int32 [sequences]
+    (the new tokens, which are in the cache already, among them).  ``scale``: default dim^-0.5.
+    ``workspace`` (uint8, bytes as ``cfwd_mx_cache_attention_workspace_size`` says) is allocated when not given.
+    """
+    torch = _torch()
+    dev, sizes, parts = _check_cache(cache)
+    if q.dim() not in (3, 4):
+        raise ValueError("q must be [sequences, heads, dim] or [sequences, tokens, heads, dim]")
+    shape, stride = q.shape, q.stride()
+    sequences, tokens, heads = shape[0], shape[1] if len(shape) == 4 else 1, shape[-2]
+    row = heads * shape[-1]  # the stride of an axis of one may be any number, and does not count
+    seq_stride = stride[0] if sequences > 1 else tokens * row
+    token_stride = stride[1] if tokens > 1 else row
+    head_stride = stride[-2] if heads > 1 else shape[-1]
+    if shape[-1] != sizes[3]:
+        raise ValueError("q has heads of %d values, the cache of %d" % (shape[-1], sizes[3]))
+    if stride[-1] != 1 and shape[-1] > 1:
+        raise ValueError("the last axis of q must be dense")
+    if q.get_device() != dev:
+        raise ValueError("tensors must be on one GPU")
+    rows, pitch = _check_table(dev, page_table)
+    if rows != sequences:
+        raise ValueError("page_table must have a row for each of %d sequences" % sequences)
+    _int32(dev, lengths, (sequences,), "lengths")
+    code = _float_code(q)
+    if out is None:
+        out = torch.empty(shape, dtype=q.dtype, device=q.device)
+    else:
+        if out.shape != shape or out.dtype != q.dtype:
+            raise ValueError("out must be as q")
+        _check_on(dev, out)
+    scale = float(scale) if scale is not None else shape[-1] ** -0.5
+    guard = _guard(dev)
+    if guard is not None:
+        with guard:
+            return mx_cache_attention(q, cache, page_table, lengths, scale, out, workspace)
+    desc, need = _mx_cache_attention_desc(dev, sizes, sequences, tokens, heads, pitch, scale, code, seq_stride,
+                                          token_stride, head_stride)
+    workspace, ws, ws_bytes = _workspace(workspace, need, q.device, dev)
+    _check(_lib().cfwd_mx_cache_attention(desc, ctypes.byref(MxCacheParts(*sizes, *parts)), q.data_ptr(),
+                                          page_table.data_ptr(), lengths.data_ptr(), out.data_ptr(), ws, ws_bytes,
+                                          _stream_of(dev)))
+    return out
+
+
+@functools.lru_cache(maxsize=1024)
+def _attention_desc(dev, *sizes):
+    """(descriptor reference, workspace bytes) on GPU ``dev``, the current one, whose CUs decide about the workspace."""
+    desc, b = AttentionDesc(*sizes), ctypes.c_size_t()
+    _check(_lib().cfwd_attention_workspace_size(ctypes.byref(desc), ctypes.byref(b)))
+    return ctypes.byref(desc), b.value
+
+
+def attention(q, k, v, q_starts, k_starts=None, causal: bool = True, scale: Optional[float] = None, out=None,
+              workspace=None):
+    """softmax(scale q k^T) v of packed prompts (cfwd_attention).
+
+    ``q`` bfloat16 [tokens, heads, dim], ``k`` and ``v`` [key tokens, kv heads, dim] with dense dims; tokens and heads may
+    be strided, as parts of one projection's output are.  Sequence i owns rows q_starts[i] .. q_starts[i + 1] - 1 of q and
+    the same of k_starts (default: q_starts) of k and v; both int32 [sequences + 1].  ``causal``: a sequence's
+    last query sees all its keys, the one before it one fewer, and so on; a query that sees none gives 0.  ``scale``:
+    default dim^-0.5.  Rows of ``out`` behind the last sequence are left as they were (undefined where the call
+    allocates it).  ``workspace`` (uint8, bytes as ``cfwd_attention_workspace_size`` says) is allocated when not given.
+    """
+    torch = _torch()
+    dev = q.get_device()
+    tokens, heads, dim, qs, qh = _heads_of(q, "q")
+    kt, kv_heads, kd, ks, kh = _heads_of(k, "k")
+    vt, vheads, vd, vs, vh = _heads_of(v, "v")
+    if kd != dim or (vt, vheads, vd) != (kt, kv_heads, kd) or not q.dtype == k.dtype == v.dtype:
+        raise ValueError("q, k and v must have one dim and dtype, k and v one shape")
+    if k.get_device() != dev or v.get_device() != dev:
+        raise ValueError("tensors must be on one GPU")
+    if k_starts is None:
+        k_starts = q_starts
+    sequences = q_starts.numel() - 1
+    if sequences < 0:
+        raise ValueError("q_starts must be int32 [sequences + 1]")
+    _int32(dev, q_starts, (sequences + 1,), "q_starts")
+    _int32(dev, k_starts, (sequences + 1,), "k_starts")
+    code = _float_code(q)
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    else:
+        if out.shape != q.shape or out.dtype != q.dtype:
+            raise ValueError("out must be as q")
+        _check_on(dev, out)
+    scale = float(scale) if scale is not None else dim ** -0.5
+    guard = _guard(dev)
+    if guard is not None:
+        with guard:
+            return attention(q, k, v, q_starts, k_starts, causal, scale, out, workspace)
+    desc, need = _attention_desc(dev, tokens, kt, sequences, heads, kv_heads, dim, int(bool(causal)), scale, code, qs, qh,
+                                 ks, kh, vs, vh)
+    workspace, ws, ws_bytes = _workspace(workspace, need, q.device, dev)
+    _check(_lib().cfwd_attention(desc, q.data_ptr(), k.data_ptr(), v.data_ptr(), q_starts.data_ptr(),
+                                 k_starts.data_ptr(), out.data_ptr(), ws, ws_bytes, _stream_of(dev)))
+    return out

@@ -6,6 +6,7 @@
 #include <cstdint>
 #include <string>
 
+#include "capi_checks.h"
 #include "gated_norm.h"
 #include "mx.h"
 
@@ -15,31 +16,6 @@ namespace {
 constexpr int kMaxK = 1 << 22;
 // Both keep the byte counts below in 63 bits: rows of the longest row, and rows at a pitch (in elements).
 constexpr long long kMaxRows = 1ll << 38, kMaxSpan = 1ll << 60;
-
-// No exception leaves the library: what is left to throw is the allocation of an error text.
-template <typename F>
-cfwd_status guarded(F f) {
-    try {
-        return f();
-    } catch (...) {
-        return CFWD_ERR_HIP;
-    }
-}
-
-cfwd_status invalid(const char* why) { return set_error(CFWD_ERR_INVALID_ARG, why); }
-
-bool aligned(const void* p, size_t to) { return reinterpret_cast<uintptr_t>(p) % to == 0; }
-size_t float_size(cfwd_dtype t) { return t == CFWD_F32 ? 4 : t == CFWD_BF16 ? 2 : 0; }
-
-struct Span {
-    const void* p;
-    unsigned long long bytes;
-};
-
-bool overlap(const Span& a, const Span& b) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
-    return a.p && b.p && a.bytes && b.bytes && x < y + b.bytes && y < x + a.bytes;
-}
 
 unsigned long long code_bytes(long long rows, long long k) { return rows * mx_code_pitch(k); }
 unsigned long long scale_bytes(long long rows, long long k) { return rows * mx_scale_pitch(k); }

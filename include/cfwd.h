@@ -460,6 +460,140 @@ cfwd_status cfwd_gated_norm(const cfwd_gated_norm_desc *desc, const void *b, con
                             const float *post_weight, const float *post_bias, const float *pre_weight,
                             const float *pre_bias, void *s, void *h, void *h_scales, void *stream);
 
+/* ---- Attention: rotary positions, a paged cache in MXFP4, attention over the
+ * cache and over packed prompts.  With the products and norms above, the other half of a
+ * transformer layer; image and video networks with attention over patches use
+ * the same calls.
+ *
+ * A tensor of heads is [tokens][heads][dim] with dense dims; its token and head
+ * strides (in elements) are the caller's, so that queries, keys and values may
+ * be parts of one projection's output.  Outputs of attention and of the cache
+ * are dense.  Integers that live on the device (positions, slots, pages,
+ * lengths, starts) are read by the kernels: values out of range never lead a
+ * memory access out of its buffer, and what they mean instead stands at each call.
+ * Nothing here allocates device memory, waits, or uses atomics: the same
+ * inputs give the same bits.  tokens or sequences may be 0: nothing is done. */
+
+/* Rotary positions.  Pair i of a head, (a, b), becomes
+ *   (a cos t - b sin t, a sin t + b cos t),   t = position[axis_i] * frequency_i,
+ * a and b being values i and i + pairs (or, adjacent, 2 i and 2 i + 1) of the
+ * head; values from 2 * pairs on stay as they are.  One table entry for each pair:
+ *   turns  frequency / (2 pi), the part of a whole turn that one position makes, as a
+ *          fraction of 2^64: the product with a position then wraps round at whole turns by
+ *          itself, and the angle is exact to 2^-32 of a turn however far the position is
+ *   axis   which of a token's positions counts; outside 0 .. axes - 1: none, the pair stays as it is
+ * (cfwd_rope_turns gives turns from a frequency.)  sin and cos are taken to 2^-23. */
+typedef struct {
+    uint64_t turns;
+    int32_t axis;
+    int32_t reserved; /* 0 */
+} cfwd_rope_pair;
+
+typedef struct {
+    long long tokens;
+    int q_heads, k_heads, head_dim; /* k_heads may be 0 */
+    int pairs, axes;                /* 2 * pairs <= head_dim */
+    int adjacent;
+    int wide_positions; /* positions are int64 [tokens][axes] instead of int32 */
+    cfwd_dtype dtype;   /* fp32 or bf16 */
+    long long q_stride, q_head_stride, k_stride, k_head_stride; /* of the inputs, in elements */
+    long long q_out_stride, q_out_head_stride, k_out_stride, k_out_head_stride;
+} cfwd_rope_desc;
+
+/* round(2^64 frequency / (2 pi)) mod 2^64 for a frequency in radians a position. */
+uint64_t cfwd_rope_turns(double frequency);
+
+/* q, k -> q_out, k_out, which may be the inputs themselves (same pointer and
+ * strides) and overlap nothing else.  table: device [pairs], 16-byte aligned.
+ * Tensors need only their element's alignment.  Enqueued on `stream`. */
+cfwd_status cfwd_rope(const cfwd_rope_desc *desc, const void *q, const void *k, const void *positions,
+                      const cfwd_rope_pair *table, void *q_out, void *k_out, void *stream);
+
+/* The paged cache: keys, and values, as MXFP4 rows [pages][heads][page_size]
+ * of head_dim values (codes and scales as above).  A token's place is its slot,
+ * page * page_size + offset; a sequence's tokens 0, 1, .. lie in the pages that its row of the
+ * page table [sequences][table_pitch] names, page_size in each. */
+typedef struct {
+    int pages, page_size, kv_heads, head_dim;
+    void *k_codes, *k_scales, *v_codes, *v_scales; /* codes 16-byte aligned, scales 4-byte */
+} cfwd_mx_cache;
+
+/* Quantises k and v [tokens][kv_heads][head_dim] (fp32 / bf16; strides for both) into the
+ * slots int32 (or wide: int64) [tokens], to the same codes as cfwd_mx_quantize.  A token whose slot is not in
+ * 0 .. pages * page_size - 1 is left out (a padded batch has -1 there).  Slots that are given must
+ * differ from each other: what a slot given twice then holds is not defined. */
+typedef struct {
+    long long tokens;
+    cfwd_dtype dtype;
+    int wide_slots;
+    long long k_stride, k_head_stride, v_stride, v_head_stride;
+} cfwd_mx_cache_write_desc;
+
+cfwd_status cfwd_mx_cache_write(const cfwd_mx_cache_write_desc *desc, const cfwd_mx_cache *cache, const void *k,
+                                const void *v, const void *slots, void *stream);
+
+/* The first tokens of every sequence back as values (exact in both types):
+ * row t of k and v [tokens][kv_heads][head_dim] is token t - starts[i] of the sequence i with
+ * starts[i] <= t < starts[i + 1] (starts: int32 [sequences + 1], from 0, never falling).
+ * Rows behind the last sequence, and rows whose page is not in 0 .. pages - 1 or not in the table, are not written. */
+typedef struct {
+    long long tokens;
+    int sequences, table_pitch;
+    cfwd_dtype dtype;
+} cfwd_mx_cache_read_desc;
+
+cfwd_status cfwd_mx_cache_read(const cfwd_mx_cache_read_desc *desc, const cfwd_mx_cache *cache, const int32_t *page_table,
+                               const int32_t *starts, void *k, void *v, void *stream);
+
+/* Attention of each sequence's newest tokens over its cache:
+ *   o = softmax(scale * q K^T) V
+ * q [sequences][tokens][q_heads][head_dim] and o are bf16; query head h reads head h / (q_heads / kv_heads)
+ * of the cache.  lengths: int32 [sequences], tokens in the cache, the new ones
+ * among them: query i sees the first length - tokens + 1 + i of them.  Lengths
+ * are taken as 0 below 0 and as table_pitch * page_size above it; tokens on pages outside 0 .. pages - 1 are not
+ * seen; a query that sees nothing gives 0.  head_dim: a multiple of 32 up to
+ * 256; page_size: a multiple of 16; tokens <= 1024; q_heads a multiple of kv_heads; q 16-byte aligned with strides
+ * that are multiples of 8 elements.
+ * Products are exact and summed in fp32, as are the softmax's sums; its weights are rounded to bf16 before the product
+ * with V. */
+typedef struct {
+    int sequences, tokens, q_heads, table_pitch;
+    float scale; /* > 0 */
+    cfwd_dtype dtype;
+    long long q_seq_stride, q_stride, q_head_stride;
+} cfwd_mx_cache_attention_desc;
+
+cfwd_status cfwd_mx_cache_attention_workspace_size(const cfwd_mx_cache_attention_desc *desc, const cfwd_mx_cache *cache,
+                                                   size_t *bytes);
+
+/* workspace: 256-byte aligned, needs no initial contents. */
+cfwd_status cfwd_mx_cache_attention(const cfwd_mx_cache_attention_desc *desc, const cfwd_mx_cache *cache, const void *q,
+                                    const int32_t *page_table, const int32_t *lengths, void *o, void *workspace,
+                                    size_t ws_bytes, void *stream);
+
+/* Attention over packed prompts: o = softmax(scale * q k^T) v for each sequence
+ * i, whose queries are rows q_starts[i] .. q_starts[i + 1] - 1 of q [q_tokens][q_heads][head_dim] and
+ * whose keys and values are rows k_starts[i] .. k_starts[i + 1] - 1 of k, v [k_tokens][kv_heads][head_dim]
+ * (starts: int32 [sequences + 1], never falling; taken as the nearest number in 0 .. tokens).
+ * causal: the last query sees every key, the one before it one fewer, and so
+ * on; a query that sees no key gives 0.  Rows of o behind the last sequence are
+ * not written.  bf16; head_dim a multiple of 8 up to 256; q_heads a multiple of kv_heads; tensors 16-byte aligned, strides
+ * multiples of 8 elements, k and v strides at most 2^24.  Roundings as in cfwd_mx_cache_attention. */
+typedef struct {
+    long long q_tokens, k_tokens;
+    int sequences, q_heads, kv_heads, head_dim;
+    int causal;
+    float scale; /* > 0 */
+    cfwd_dtype dtype;
+    long long q_stride, q_head_stride, k_stride, k_head_stride, v_stride, v_head_stride;
+} cfwd_attention_desc;
+
+cfwd_status cfwd_attention_workspace_size(const cfwd_attention_desc *desc, size_t *bytes);
+
+cfwd_status cfwd_attention(const cfwd_attention_desc *desc, const void *q, const void *k, const void *v,
+                           const int32_t *q_starts, const int32_t *k_starts, void *o, void *workspace, size_t ws_bytes,
+                           void *stream);
+
 /* Static description of a status code. */
 const char *cfwd_status_string(cfwd_status status);
 
