@@ -39,7 +39,7 @@ COMMON = [
 
 
 # Per-source extra flags.  The stem kernels (gather form and the int8 NCHW4
-# stem) and the persistent int8 kernel are bound by vector ALU issue; keeping
+# stem), the persistent int8 kernel and the attention kernels are bound by vector ALU issue; keeping
 # MFMA results in ordinary VGPRs instead of accumulation registers removes the
 # register moves around their epilogues (about a tenth of their vector
 # instructions) without raising register use (in the persistent kernel it
@@ -49,6 +49,8 @@ EXTRA = {
     "k_lowc.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
     "k_stem_i8.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
     "k_igemm_i8_stream.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+    "k_attention.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+    "k_mx_decode.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
 }
 
 

@@ -2,22 +2,35 @@
 //
 //   o = softmax(scale * q k^T) v
 //
-// A workgroup takes 128 RB rows of one head of keys and values, a row being a (token,
+// A workgroup takes 128 rows of one head of keys and values, a row being a (token,
 // query head) of the group that shares it: grouped heads read their keys once,
 // and a tile of rows spans few tokens, which wastes little at the causal edge.
-// Keys and values come 64 at a time through LDS, by copies that bypass the
-// registers, STAGES deep.  S^T = k q^T has a query in each lane's column and 16 keys
-// in its registers, which is how P^T enters O^T = v^T P^T: only the row's maximum
-// and sum pass between lanes (two of them hold a row).  v^T comes out of LDS by transposing reads.
-// With m the running maximum, O and l are multiplied by 2^(m - m') only
-// where a score passes m by more than 2^8: until then weights up to 2^8 are as
-// good.  A row goes by its own scores alone, so that its result does not depend on the others'.
+// Each of its four waves has 32 rows.  Keys and values come 64 at a time through
+// LDS, by copies that bypass the registers.  S^T = k q^T has a query in each
+// lane's column and 16 of 32 keys in its registers, which is how P^T enters
+// O^T = v^T P^T: only the row's sum passes between lanes (two of them hold a row).
+// v^T comes out of LDS by transposing reads.
+//
+// Softmax.  Weights are 2^(s - m) with s in units of log2 and m no running maximum
+// but any number that the scores have not passed by far: it moves only where a
+// lane's 16 weights sum up to more than 2^12, then to the row's largest score, and
+// O and l are multiplied by 2^(m - m').  Weights have bf16's 8 bits at any size, so
+// nothing is lost, and no maximum is taken otherwise: sixteen instructions for every 64 keys and a
+// chain of latencies before the weights less (16384 tokens: 2010 us with the
+// maxima, 1960 without).  A row goes by its own scores alone, so that its result
+// does not depend on the others'.
+//
+// A wave issues a vector instruction at most every eight cycles or so, alone on its SIMD or not, and a
+// matrix instruction takes 32.  So no phase is left without either: while the matrix cores take the scores of the next 32
+// keys, half of this half's weights are computed, and the other half of the next ones' while they multiply by the values.
+// Two waves a SIMD (three for heads of 64) fill what is left.
 //
 // Few rows over many keys are split over the keys; a second launch joins the parts.
 #include "attention.h"
 #include "mx.h"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace cfwd {
 namespace fa {
@@ -30,7 +43,7 @@ typedef __attribute__((address_space(3))) u32x4_t lds_u32x4;
 
 constexpr int BN = 64;          // keys of a tile
 constexpr float kLow = -3.0e38f;  // m before any score: finite, so that differences are numbers
-constexpr float kSlack = 8.0f;
+constexpr float kMost = 4096.0f;  // a lane's 16 weights sum up to this before m follows the scores
 
 struct Params {
     const bf16_t *q, *k, *v;
@@ -44,8 +57,12 @@ struct Params {
     Divisor per_group;
 };
 
+// Copies 16 bytes a lane from a buffer straight to LDS, lane after lane from `lds` on (the same for the wave);
+// out-of-range lanes write 0.  The compiler does not see these loads: wait_loads() and a barrier come before the data
+// are read.  It may have moved the buffer's words to scalar registers with vector instructions, which a load must not
+// follow closer than five wait states.
 __device__ __forceinline__ void load_to_lds16(const __amdgpu_buffer_rsrc_t& b, uint32_t off, uint32_t lds) {
-    asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" : : "{m0}"(lds), "v"(off), "s"(b) : "memory");
+    asm volatile("s_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" : : "{m0}"(lds), "v"(off), "s"(b) : "memory");
 }
 template <int N>
 __device__ __forceinline__ void wait_loads() {  // until at most N of this wave's loads are outstanding
@@ -54,8 +71,15 @@ __device__ __forceinline__ void wait_loads() {  // until at most N of this wave'
 // All waves of the workgroup, each with its reads of LDS done: what they read may then be overwritten.
 __device__ __forceinline__ void barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void* p, uint32_t bytes) {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, static_cast<int>(bytes), 0x00020000);
+// A number that is the same for the whole wave, in scalar registers.
+__device__ __forceinline__ uint64_t uniform(uint64_t a) {
+    const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(a));
+    const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(a >> 32));
+    return static_cast<uint64_t>(hi) << 32 | lo;
+}
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(uint64_t p, uint32_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(uniform(p)), 0, __builtin_amdgcn_readfirstlane(bytes),
+                                             0x00020000);
 }
 
 __device__ __forceinline__ f32x16 mma(const u32x4_t& a, const u32x4_t& b, const f32x16& c) {
@@ -69,12 +93,17 @@ __device__ __forceinline__ int k_swizzle(int row) { return DP == 64 ? (row >> 1)
 template <int DP>
 __device__ __forceinline__ int v_swizzle(int row) { return DP == 64 ? ((row >> 1) & 1) * 4 : (row & 3) * 4; }
 
+// Rows of a sequence; the same for the whole wave.
 struct Range {
     int from, count;
 };
+__device__ __forceinline__ int count_of(const int32_t* starts, int seq, int tokens) {
+    const int a = min(max(starts[seq], 0), tokens);
+    return min(max(starts[seq + 1], a), tokens) - a;
+}
 __device__ __forceinline__ Range rows_of(const int32_t* starts, int seq, int tokens) {
     const int a = min(max(starts[seq], 0), tokens), b = min(max(starts[seq + 1], a), tokens);
-    return {a, b - a};
+    return {__builtin_amdgcn_readfirstlane(a), __builtin_amdgcn_readfirstlane(b - a)};
 }
 
 // The sequence of the tile `tile`, counted from the last one back, and its tile; seq < 0: there is none.
@@ -86,7 +115,7 @@ __device__ Place find_tile(const Params& p, int tile, int lane) {
     int total = 0;
     for (int s = 0; s < p.sequences; s += 64) {
         int n = 0;
-        if (s + lane < p.sequences) n = (rows_of(p.q_starts, s + lane, p.q_tokens).count * p.group + BM - 1) / BM;
+        if (s + lane < p.sequences) n = (count_of(p.q_starts, s + lane, p.q_tokens) * p.group + BM - 1) / BM;
         total += n;
     }
 #pragma unroll
@@ -96,7 +125,7 @@ __device__ Place find_tile(const Params& p, int tile, int lane) {
     int before = 0;
     for (int s = 0; s < p.sequences; s += 64) {
         int n = 0;
-        if (s + lane < p.sequences) n = (rows_of(p.q_starts, s + lane, p.q_tokens).count * p.group + BM - 1) / BM;
+        if (s + lane < p.sequences) n = (count_of(p.q_starts, s + lane, p.q_tokens) * p.group + BM - 1) / BM;
         int upto = n;
 #pragma unroll
         for (int d = 1; d < 64; d *= 2) {
@@ -114,11 +143,14 @@ __device__ Place find_tile(const Params& p, int tile, int lane) {
     return {-1, 0};
 }
 
-template <int DP, int NK, int NV, int RB, int STAGES, int RESIDENT>
-__global__ __launch_bounds__(256, RESIDENT) void kernel(Params p) {
-    constexpr int BM = 128 * RB, PIECES = DP / 8, TILE = BN * DP * 2;
-    constexpr int COPIES = BN * PIECES / 256;  // of 16 bytes, a thread and tile
-    __shared__ __attribute__((aligned(1024))) uint8_t area[STAGES * 2 * TILE];
+template <int N>
+using Int = std::integral_constant<int, N>;
+
+template <int DP, int NK, int NV, int WAVES, int KS, int VS, int SIMD_WAVES>
+__global__ __launch_bounds__(64 * WAVES, SIMD_WAVES) void kernel(Params p) {
+    constexpr int BM = 32 * WAVES, PIECES = DP / 8, TILE = BN * DP * 2, HALF = TILE / 2;
+    constexpr int COPIES = BN * PIECES / (64 * WAVES);  // of 16 bytes, a thread and tile
+    __shared__ __attribute__((aligned(1024))) uint8_t area[(KS + VS) * TILE];  // KS tiles of keys, then VS of values
     const uint32_t lds = static_cast<uint32_t>(
         reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t*)area));
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -135,179 +167,293 @@ __global__ __launch_bounds__(256, RESIDENT) void kernel(Params p) {
     const int last_token = divide(min(row0 + BM, rows) - 1, p.per_group);
     const int keys = p.causal ? min(max(offset + last_token + 1, 0), ks.count) : ks.count;
     const int all_tiles = (keys + BN - 1) / BN;
-    const int t0 = static_cast<int>(static_cast<long long>(blockIdx.y) * all_tiles / p.splits);
-    const int t1 = static_cast<int>(static_cast<long long>(blockIdx.y + 1) * all_tiles / p.splits);
+    const int t0 = __builtin_amdgcn_readfirstlane(static_cast<int>(static_cast<long long>(blockIdx.y) * all_tiles / p.splits));
+    const int t1 = __builtin_amdgcn_readfirstlane(static_cast<int>((blockIdx.y + 1ll) * all_tiles / p.splits));
 
     // this wave's rows
-    const int wave0 = row0 + wave * 32 * RB;
-    int seen[RB];
-    u32x4_t q[RB][NK];
-#pragma unroll
-    for (int r = 0; r < RB; ++r) {
-        const int row = min(wave0 + r * 32 + n, rows - 1);
-        const int token = divide(row, p.per_group);
-        seen[r] = p.causal ? min(offset + token + 1, ks.count) : ks.count;
+    const int wave0 = row0 + wave * 32;
+    const int row = min(wave0 + n, rows - 1), token = divide(row, p.per_group);
+    const int end = __builtin_amdgcn_readfirstlane(min(t1 * BN, ks.count));  // of this split's keys
+    const int seen = p.causal ? min(offset + token + 1, end) : end;
+    u32x4_t q[NK];
+    {
         const bf16_t* x = p.q + (qs.from + token) * p.q_stride + (head * p.group + row - token * p.group) * p.q_head_stride;
 #pragma unroll
         for (int c = 0; c < NK; ++c) {
             const int d = 16 * c + 8 * h;
-            q[r][c] = d < p.dim ? *reinterpret_cast<const u32x4_t*>(x + d) : u32x4_t{0, 0, 0, 0};
+            q[c] = d < p.dim ? *reinterpret_cast<const u32x4_t*>(x + d) : u32x4_t{0, 0, 0, 0};
         }
     }
     const int first_token = divide(min(wave0, rows - 1), p.per_group);
-    const int least = p.causal ? min(offset + first_token + 1, ks.count) : ks.count;  // every row of the wave sees these
-    const int wave_last = divide(min(wave0 + 32 * RB, rows) - 1, p.per_group);
-    const int most = wave0 >= rows ? 0 : p.causal ? min(offset + wave_last + 1, ks.count) : ks.count;
+    const int least = p.causal ? min(offset + first_token + 1, end) : end;  // every row of the wave sees these
+    const int wave_last = divide(min(wave0 + 32, rows) - 1, p.per_group);
+    const int most = wave0 >= rows ? 0 : p.causal ? min(max(offset + wave_last + 1, 0), end) : end;
+    const int wave_t1 = (most + BN - 1) / BN;
 
-    // copies: piece i * 256 + thread of a tile, from the place that the permutation puts there; outside dim: nothing
+    // copies: piece i * threads + thread of a tile, from the place that the permutation puts there; outside dim: nothing
     uint32_t k_off[COPIES], v_off[COPIES];
+    const uint32_t k_row = static_cast<uint32_t>(p.k_stride) * 2, v_row = static_cast<uint32_t>(p.v_stride) * 2;  // bytes
 #pragma unroll
     for (int i = 0; i < COPIES; ++i) {
-        const int at = i * 256 + threadIdx.x, row = at / PIECES, piece = at % PIECES;
-        const int kp = piece ^ k_swizzle<DP>(row), vp = piece ^ v_swizzle<DP>(row);
-        k_off[i] = kp * 8 < p.dim ? static_cast<uint32_t>(row * p.k_stride + kp * 8) * 2 : 0xfffffff0u;
-        v_off[i] = vp * 8 < p.dim ? static_cast<uint32_t>(row * p.v_stride + vp * 8) * 2 : 0xfffffff0u;
+        const int at = i * 64 * WAVES + threadIdx.x, r = at / PIECES, piece = at % PIECES;
+        const int kp = piece ^ k_swizzle<DP>(r), vp = piece ^ v_swizzle<DP>(r);
+        k_off[i] = kp * 8 < p.dim ? r * k_row + kp * 16 : 0xfffffff0u;
+        v_off[i] = vp * 8 < p.dim ? r * v_row + vp * 16 : 0xfffffff0u;
     }
-    const bf16_t* kbase = p.k + ks.from * p.k_stride + head * p.k_head_stride;
-    const bf16_t* vbase = p.v + ks.from * p.v_stride + head * p.v_head_stride;
-    auto copy = [&](int t) __attribute__((always_inline)) {
-        // rows from the sequence's end on are out of the buffer's range and become zeros
-        const int left = t < t1 ? min(ks.count - t * BN, BN) : 0;
-        const uint32_t to = lds + (t % STAGES) * 2 * TILE + wave * 1024;
-        const auto kb = buffer(kbase + static_cast<long long>(t) * BN * p.k_stride, left * static_cast<uint32_t>(p.k_stride) * 2);
-        const auto vb = buffer(vbase + static_cast<long long>(t) * BN * p.v_stride, left * static_cast<uint32_t>(p.v_stride) * 2);
+    const uint64_t k_base = uniform(reinterpret_cast<uint64_t>(p.k + ks.from * p.k_stride + head * p.k_head_stride));
+    const uint64_t v_base = uniform(reinterpret_cast<uint64_t>(p.v + ks.from * p.v_stride + head * p.v_head_stride));
+    const uint32_t lds_wave = lds + wave * 1024;
+    // rows from the end on are out of the buffer's range and become zeros
+    auto copy = [&](uint64_t base, uint32_t row_bytes, const uint32_t(&off)[COPIES], int key, uint32_t to) __attribute__((always_inline)) {
+        int left = end - key;
+        left = left < 0 ? 0 : left;
+        left = left > BN ? BN : left;
+        const auto b = buffer(base + static_cast<uint64_t>(static_cast<uint32_t>(key)) * row_bytes, left * row_bytes);
 #pragma unroll
-        for (int i = 0; i < COPIES; ++i) load_to_lds16(kb, k_off[i], to + i * 4096);
+        for (int i = 0; i < COPIES; ++i) load_to_lds16(b, off[i], lds_wave + to + i * WAVES * 1024);
+    };
+    auto copy_k = [&](int key, int slot) __attribute__((always_inline)) { copy(k_base, k_row, k_off, key, slot * TILE); };
+    auto copy_v = [&](int key, int slot) __attribute__((always_inline)) { copy(v_base, v_row, v_off, key, (KS + slot) * TILE); };
+
+    // places of a lane's reads in a tile; those of other tiles differ by constants, which the reads hold.  Of keys, piece
+    // 2 c + h of row n; of values, four lanes point at 16 values of each of four keys (a lane then gets one value of all four).
+    uint32_t k_at[NK], v_at[NV];
 #pragma unroll
-        for (int i = 0; i < COPIES; ++i) load_to_lds16(vb, v_off[i], to + TILE + i * 4096);
+    for (int c = 0; c < NK; ++c) {
+        k_at[c] = lds + n * DP * 2 + ((2 * c + h) ^ k_swizzle<DP>(n)) * 16;
+        asm volatile("" : "+v"(k_at[c]));
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int in = lane & 15, r = 4 * h + (in >> 2), d = 32 * i + 16 * ((lane >> 4) & 1) + 4 * (in & 3);
+        v_at[i] = lds + KS * TILE + r * DP * 2 + ((d >> 3) ^ v_swizzle<DP>(r)) * 16 + (d & 7) * 2;
+        asm volatile("" : "+v"(v_at[i]));
+    }
+
+    f32x16 o[NV], score[2];
+    u32x4_t kf[NK];
+    float m = kLow, l = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) o[i][j] = 0.0f;
+
+    auto mask = [&](f32x16& s, int key) __attribute__((always_inline)) {
+        asm volatile("");  // a branch around this stays one: selecting every score would cost half as much as the softmax
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+            if (key + 8 * (j / 4) + 4 * h + j % 4 >= seen) s[j] = -__builtin_inff();
     };
 
-    f32x16 o[RB][NV];
-    float m[RB], l[RB];
+    // The weights of pair w of a half's scores, and their sum.  It takes the weights as they enter the product: rounded.
+    auto weigh = [&](const f32x16& s, int w, float(&e)[2]) __attribute__((always_inline)) {
+        e[0] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[2 * w], p.scale2, -m));
+        e[1] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[2 * w + 1], p.scale2, -m));
+    };
+    auto pack = [&](const float(&e)[2], uint32_t& weight, float& sum) __attribute__((always_inline)) {
+        weight = pack_bf16x2(e[0], e[1]);
+        sum = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2_t, weight), __builtin_bit_cast(bf16x2_t, 0x3f803f80u), sum, false);
+    };
+    // One step: while the matrix cores take the scores of the half that follows (from key next_key on; its keys are in kf),
+    // the later weights of half B of the tile in slot V; while they take the product of the weights and B's values, the
+    // earlier weights of the half that follows.  The keys of the half after it are K bytes into the keys' area.
+    uint32_t early[4];
+    float early_sum = 0.0f;
+    bool not_finite = false;  // a value that is NaN or infinite was taken out
+    auto step = [&](auto which, auto v_slot, auto k_after, int next_key, auto between) __attribute__((always_inline)) {
+        constexpr int B = decltype(which)::value, V = decltype(v_slot)::value * TILE, K = decltype(k_after)::value;
+        f32x16& cur = score[B];
+        f32x16& nxt = score[1 - B];
+        u32x4_t vf[2][NV];
+        uint32_t weight[8] = {early[0], early[1], early[2], early[3]};
+        float e[4][2], sum = early_sum;
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int r = 0; r < RB; ++r) {
-        m[r] = kLow;
-        l[r] = 0.0f;
+        for (int c = 0; c < NK; ++c) {
+            if (c == 0)
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
+                for (int j = 0; j < 16; ++j) nxt[j] = 0.0f;
+            nxt = mma(kf[c], q[c], nxt);
 #pragma unroll
-            for (int j = 0; j < 16; ++j) o[r][i][j] = 0.0f;
-    }
+            for (int r = 2 * NV * c / NK; r < 2 * NV * (c + 1) / NK; ++r)
+#pragma unroll
+                for (int part = 0; part < 2; ++part) {  // 16 keys: 16 (r / NV) + 4 h + (0 .. 3) and 8 on
+                    const uint2 x = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                        reinterpret_cast<lds_s16x4*>(v_at[r % NV] + V + (32 * B + 16 * (r / NV) + 8 * part) * DP * 2)));
+                    vf[r / NV][r % NV][2 * part] = x.x;
+                    vf[r / NV][r % NV][2 * part + 1] = x.y;
+                }
+            // the last products have no weights beside them: they cover the way from the sum to the branch
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (i * NK / 6 == c) weigh(cur, 4 + i, e[i]);
+                if (i * NK / 6 + 1 == c) pack(e[i], weight[4 + i], sum);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        asm volatile("" : "+v"(weight[4]), "+v"(weight[5]), "+v"(weight[6]), "+v"(weight[7]), "+v"(sum));  // all before the branch
+        if (__any(!(sum <= kMost))) {
+            // scores far above m (or the first ones, or NaN): m moves up to the row's largest, and the weights are taken again
+            float top = cur[0];
+#pragma unroll
+            for (int j = 1; j < 16; ++j) top = fmaxf(top, cur[j]);
+            top = fmaxf(top, __shfl_xor(top, 32)) * p.scale2;
+            const float other = __shfl_xor(sum, 32);
+            const float to = (!(sum <= kMost) || !(other <= kMost)) && top > m ? top : m, f = __builtin_amdgcn_exp2f(m - to);
+            m = to;
+            l *= f;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) o[i] *= f;
+            sum = 0.0f;
+#pragma unroll
+            for (int w = 0; w < 8; ++w) {
+                weigh(cur, w, e[0]);
+                pack(e[0], weight[w], sum);
+            }
+        }
+        l += sum;
+        if (p.causal && next_key > least) {
+            // Some rows see keys of this half that others do not, and a weight of 0 does not undo a NaN or an infinity among
+            // the values: those are taken out, and added at the end where they are seen.
+            asm volatile("");
+            typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+            u16x2 largest = {0, 0};
+#pragma unroll
+            for (int r = 0; r < 2 * NV; ++r)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    largest = __builtin_elementwise_max(largest, __builtin_bit_cast(u16x2, vf[r / NV][r % NV][j] & 0x7fff7fffu));
+            if (__any(largest[0] >= 0x7f80 || largest[1] >= 0x7f80)) {
+                not_finite = true;
+#pragma unroll
+                for (int r = 0; r < 2 * NV; ++r)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t x = vf[r / NV][r % NV][j];
+                        vf[r / NV][r % NV][j] = x & ((x & 0x7f80u) == 0x7f80u ? 0xffff0000u : ~0u) &
+                                                ((x & 0x7f800000u) == 0x7f800000u ? 0x0000ffffu : ~0u);
+                    }
+            }
+        }
+        between();
+        if (next_key + BN / 2 > least) mask(nxt, next_key);
+        early_sum = 0.0f;
+        constexpr int M = 2 * NV;
+#pragma unroll
+        for (int x = 0; x < M; ++x) {
+            const u32x4_t w = {weight[x / NV * 4], weight[x / NV * 4 + 1], weight[x / NV * 4 + 2], weight[x / NV * 4 + 3]};
+            o[x % NV] = mma(vf[x / NV][x % NV], w, o[x % NV]);
+#pragma unroll
+            for (int c = NK * x / M; c < NK * (x + 1) / M; ++c) kf[c] = *reinterpret_cast<lds_u32x4*>(k_at[c] + K);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (1 + i * M / 6 == x) weigh(nxt, i, e[i]);
+                if (2 + i * M / 6 == x || (x == M - 1 && 2 + i * M / 6 == M)) pack(e[i], early[i], early_sum);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        asm volatile("" : "+v"(early[0]), "+v"(early[1]), "+v"(early[2]), "+v"(early[3]), "+v"(early_sum));
+    };
 
-    for (int s = 0; s < STAGES - 1; ++s) copy(t0 + s);
-    for (int t = t0; t < t1; ++t) {
-        wait_loads<(STAGES - 2) * 2 * COPIES>();
-        barrier();  // tile t is whole, and tile t - 1's stage is free
-        copy(t + STAGES - 1);
-        if (t * BN >= most) continue;
-        const uint32_t kt = lds + (t % STAGES) * 2 * TILE, vt = kt + TILE;
-        f32x16 score[RB][2];
+    // Tiles of keys in LDS lie half a tile behind those of values: tile t's steps need the keys of its second half and of
+    // the next tile's first.  The very first half comes in the slot of values that is filled last.
+    copy(k_base, k_row, k_off, t0 * BN, (KS + VS - 1) * TILE);
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
+    for (int s = 0; s < KS || s < VS - 1; ++s) {
+        if (s < KS) copy_k((t0 + s) * BN + BN / 2, s);
+        if (s < VS - 1) copy_v((t0 + s) * BN, s);
+    }
+    // here q has arrived: a wait inside the loop would also be one for the copies that are on their way
 #pragma unroll
-            for (int r = 0; r < RB; ++r)
+    for (int c = 0; c < NK; ++c) asm volatile("" : "+v"(q[c]));
+    wait_loads<(KS + VS - 3) * COPIES>();
+    barrier();
+    if (t0 < wave_t1) {
 #pragma unroll
-                for (int j = 0; j < 16; ++j) score[r][b][j] = 0.0f;
-            const int row = 32 * b + n;
+        for (int c = 0; c < NK; ++c) kf[c] = *reinterpret_cast<lds_u32x4*>(k_at[c] + (KS + VS - 1) * TILE);
 #pragma unroll
-            for (int c = 0; c < NK; ++c) {
-                const u32x4_t f = *reinterpret_cast<lds_u32x4*>(kt + row * DP * 2 + ((2 * c + h) ^ k_swizzle<DP>(row)) * 16);
+        for (int j = 0; j < 16; ++j) score[0][j] = 0.0f;
 #pragma unroll
-                for (int r = 0; r < RB; ++r) score[r][b] = mma(f, q[r][c], score[r][b]);
-            }
+        for (int c = 0; c < NK; ++c) score[0] = mma(kf[c], q[c], score[0]);
+        mask(score[0], t0 * BN);
+#pragma unroll
+        for (int c = 0; c < NK; ++c) kf[c] = *reinterpret_cast<lds_u32x4*>(k_at[c]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float e[2];
+            weigh(score[0], i, e);
+            pack(e, early[i], early_sum);
         }
-        if (t * BN + BN > least) {
-#pragma unroll
-            for (int b = 0; b < 2; ++b)
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const int key = t * BN + 32 * b + 8 * (j / 4) + 4 * h + j % 4;
-#pragma unroll
-                    for (int r = 0; r < RB; ++r)
-                        if (key >= seen[r]) score[r][b][j] = -__builtin_inff();
-                }
+    }
+    // Tile t, the u-th of a round over all slots.  Its turn, between the last scores that its keys give and the product with
+    // its last values: the next tile is whole, and the slots of its keys and of the values before it are free.
+    auto tile = [&](int t, auto round) __attribute__((always_inline)) {
+        constexpr int U = decltype(round)::value, TURNS = KS - 1 < VS - 2 ? KS - 1 : VS - 2;
+        auto turn = [&]() __attribute__((always_inline)) {
+            wait_loads<(TURNS - 1) * 2 * COPIES>();
+            barrier();
+            copy_k((t + KS) * BN + BN / 2, U % KS);
+            copy_v((t + VS - 1) * BN, (U + VS - 1) % VS);
+        };
+        if (t >= wave_t1) {
+            turn();
+            return;
         }
-        u32x4_t weight[RB][4];
-#pragma unroll
-        for (int r = 0; r < RB; ++r) {
-            float top = score[r][0][0];
-#pragma unroll
-            for (int j = 1; j < 32; ++j) top = fmaxf(top, score[r][j / 16][j % 16]);
-            top *= p.scale2;
-            if (__any(top > m[r] + kSlack)) {
-                top = fmaxf(top, __shfl_xor(top, 32));
-                const float to = top > m[r] + kSlack ? top : m[r], f = __builtin_amdgcn_exp2f(m[r] - to);
-                m[r] = to;
-                l[r] *= f;
-#pragma unroll
-                for (int i = 0; i < NV; ++i) o[r][i] *= f;
-            }
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(score[r][i / 8][2 * i % 16], p.scale2, -m[r]));
-                const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(score[r][i / 8][2 * i % 16 + 1], p.scale2, -m[r]));
-                const uint32_t w = pack_bf16x2(e0, e1);
-                weight[r][i / 4][i % 4] = w;
-                // the sum takes the weights as they enter the product: rounded
-                l[r] = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2_t, w),
-                                                       __builtin_bit_cast(bf16x2_t, 0x3f803f80u), l[r], false);
-            }
-        }
-#pragma unroll
-        for (int c = 0; c < 4; ++c)  // 16 keys: 16 c + 4 h + (0 .. 3) and 8 on
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                u32x4_t f;
-#pragma unroll
-                for (int part = 0; part < 2; ++part) {
-                    // four lanes point at 16 values of each of four keys; a lane gets one value of all four
-                    const int in = lane & 15, row = 16 * c + 8 * part + 4 * h + (in >> 2);
-                    const int d = 32 * i + 16 * ((lane >> 4) & 1) + 4 * (in & 3);
-                    const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_s16x4*>(
-                        vt + row * DP * 2 + ((d >> 3) ^ v_swizzle<DP>(row)) * 16 + (d & 7) * 2));
-                    const uint2 y = __builtin_bit_cast(uint2, x);
-                    f[2 * part] = y.x;
-                    f[2 * part + 1] = y.y;
-                }
-#pragma unroll
-                for (int r = 0; r < RB; ++r) o[r][i] = mma(f, weight[r][c], o[r][i]);
-            }
+        step(Int<0>{}, Int<U % VS>{}, Int<U % KS * TILE + HALF>{}, t * BN + BN / 2, [] {});
+        step(Int<1>{}, Int<U % VS>{}, Int<(U + 1) % KS * TILE>{}, t * BN + BN, turn);
+    };
+    constexpr int ROUND = KS == VS ? KS : KS * VS;
+    static_assert(KS == 2 || KS == 4, "the slots of a round");
+    for (int t = t0; t < t1; t += ROUND) {
+        tile(t, Int<0>{});
+        if (t + 1 < t1) tile(t + 1, Int<1>{});
+        if (ROUND > 2 && t + 2 < t1) tile(t + 2, Int<2 % ROUND>{});
+        if (ROUND > 3 && t + 3 < t1) tile(t + 3, Int<3 % ROUND>{});
+        if (ROUND > 4 && t + 4 < t1) tile(t + 4, Int<4 % ROUND>{});
+        if (ROUND > 5 && t + 5 < t1) tile(t + 5, Int<5 % ROUND>{});
     }
     wait_loads<0>();  // none is left on its way to LDS that the next workgroup may own
 
-#pragma unroll
-    for (int r = 0; r < RB; ++r) {
-        l[r] += __shfl_xor(l[r], 32);
-        const int row = wave0 + r * 32 + n;
-        if (row >= rows) continue;
-        const int token = divide(row, p.per_group);
-        const long long at = static_cast<long long>(qs.from + token) * p.heads + head * p.group + row - token * p.group;
-        if (p.splits == 1) {
-            const float inverse = l[r] == 0.0f ? 0.0f : 1.0f / l[r];
+    l += __shfl_xor(l, 32);
+    if (not_finite) {
+        const bf16_t* x = p.v + ks.from * p.v_stride + head * p.v_head_stride;
+        for (int key = max(least & ~(BN / 2 - 1), t0 * BN); key < min(seen, end); ++key)
 #pragma unroll
             for (int i = 0; i < NV; ++i)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int d = 32 * i + 8 * j + 4 * h;
-                    if (d >= p.dim) continue;
-                    uint2 y;
-                    y.x = pack_bf16x2(o[r][i][4 * j] * inverse, o[r][i][4 * j + 1] * inverse);
-                    y.y = pack_bf16x2(o[r][i][4 * j + 2] * inverse, o[r][i][4 * j + 3] * inverse);
-                    *reinterpret_cast<uint2*>(p.o + at * p.dim + d) = y;
+                for (int j = 0; j < 16; ++j) {
+                    const int d = 32 * i + 8 * (j / 4) + 4 * h + j % 4;
+                    const float y = d < p.dim ? bf16_to_float(x[key * p.v_stride + d].bits) : 0.0f;
+                    if (!(__builtin_fabsf(y) < __builtin_inff())) o[i][j] += y;
                 }
-        } else {
-            const long long to = at * p.splits + blockIdx.y;
-            if (h == 0) *reinterpret_cast<float2*>(p.part_ml + 2 * to) = make_float2(m[r], l[r]);
+    }
+    if (wave0 + n >= rows) return;
+    const long long at = static_cast<long long>(qs.from + token) * p.heads + head * p.group + row - token * p.group;
+    if (p.splits == 1) {
+        const float inverse = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
+        for (int i = 0; i < NV; ++i)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int d = 32 * i + 8 * j + 4 * h;
-                    if (d < p.dim)
-                        *reinterpret_cast<f32x4*>(p.part + to * p.dim + d) =
-                            f32x4{o[r][i][4 * j], o[r][i][4 * j + 1], o[r][i][4 * j + 2], o[r][i][4 * j + 3]};
-                }
-        }
+            for (int j = 0; j < 4; ++j) {
+                const int d = 32 * i + 8 * j + 4 * h;
+                if (d >= p.dim) continue;
+                uint2 y;
+                y.x = pack_bf16x2(o[i][4 * j] * inverse, o[i][4 * j + 1] * inverse);
+                y.y = pack_bf16x2(o[i][4 * j + 2] * inverse, o[i][4 * j + 3] * inverse);
+                *reinterpret_cast<uint2*>(p.o + at * p.dim + d) = y;
+            }
+    } else {
+        const long long to = at * p.splits + blockIdx.y;
+        if (h == 0) *reinterpret_cast<float2*>(p.part_ml + 2 * to) = make_float2(m, l);
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int d = 32 * i + 8 * j + 4 * h;
+                if (d < p.dim)
+                    *reinterpret_cast<f32x4*>(p.part + to * p.dim + d) =
+                        f32x4{o[i][4 * j], o[i][4 * j + 1], o[i][4 * j + 2], o[i][4 * j + 3]};
+            }
     }
 }
 
@@ -339,7 +485,7 @@ __global__ __launch_bounds__(256) void join_kernel(Params p, Divisor across, uin
 }
 
 struct Plan {
-    int rb, splits;
+    int splits;
     long long tiles;  // upper bound
     size_t part_bytes, bytes;
 };
@@ -347,9 +493,9 @@ struct Plan {
 Plan plan(const cfwd_attention_desc* d) {
     Plan r{};
     const long long group = d->q_heads / d->kv_heads, cus = compute_units();
-    auto tiles = [&](int bm) { return std::max(1ll, d->q_tokens * group / bm + std::min<long long>(d->sequences, d->q_tokens)); };
-    r.rb = d->head_dim <= 128 && tiles(256) * d->kv_heads >= cus ? 2 : 1;
-    r.tiles = tiles(128 * r.rb);
+    // sequences of x rows in all have at most (x + n (bm - 1)) / bm tiles, n of them not empty
+    auto tiles = [&](int bm) { return (d->q_tokens * group + std::min<long long>(d->sequences, d->q_tokens) * (bm - 1)) / bm; };
+    r.tiles = tiles(128);
     const long long keys = d->k_tokens / std::max(1, d->sequences);
     r.splits = static_cast<int>(std::max(1ll, std::min({2 * cus / (r.tiles * d->kv_heads), keys / 256, 64ll})));
     if (r.splits > 1) {
@@ -394,19 +540,11 @@ cfwd_status attention(const cfwd_attention_desc* d, const void* q, const void* k
     p.v_head_stride = d->v_head_stride;
     p.per_group = mx::divisor(p.group);
     const dim3 grid(static_cast<unsigned>(plan.tiles * p.kv_heads), plan.splits);
-    auto go = [&](auto kernel) { kernel<<<grid, 256, 0, st>>>(p); };
-    if (p.dim <= 64) {
-        if (plan.rb == 1) go(fa::kernel<64, 4, 2, 1, 3, 2>);
-        else go(fa::kernel<64, 4, 2, 2, 4, 1>);
-    } else if (p.dim <= 96) {
-        if (plan.rb == 1) go(fa::kernel<128, 6, 3, 1, 2, 2>);
-        else go(fa::kernel<128, 6, 3, 2, 4, 1>);
-    } else if (p.dim <= 128) {
-        if (plan.rb == 1) go(fa::kernel<128, 8, 4, 1, 2, 2>);
-        else go(fa::kernel<128, 8, 4, 2, 4, 1>);
-    } else {
-        go(fa::kernel<256, 16, 8, 1, 2, 1>);
-    }
+    auto go = [&](auto kernel, int waves) { kernel<<<grid, 64 * waves, 0, st>>>(p); };
+    if (p.dim <= 64) go(fa::kernel<64, 4, 2, 4, 2, 3, 3>, 4);
+    else if (p.dim <= 96) go(fa::kernel<128, 6, 3, 4, 2, 3, 2>, 4);
+    else if (p.dim <= 128) go(fa::kernel<128, 8, 4, 4, 2, 3, 2>, 4);
+    else go(fa::kernel<256, 16, 8, 4, 2, 3, 1>, 4);
     const cfwd_status e = check_hip(hipGetLastError(), "attention launch");
     if (e != CFWD_OK || plan.splits == 1) return e;
     const long long units = d->q_tokens * d->q_heads * (d->head_dim / 4);  // split only where rows are few

@@ -387,3 +387,33 @@ def test_attention_starts_out_of_range():
     torch.cuda.synchronize()
     assert B.attention(q[:0], k, k, ints(torch, [0, 0]), ints(torch, [0, 60])).shape == (0, 2, 64)
     assert not B.attention(q, k[:0], k[:0], ints(torch, [0, 50]), ints(torch, [0, 0])).any()
+
+
+@pytest.mark.parametrize("dim", [64, 80, 128, 256])
+def test_attention_values_that_are_not_finite(dim):
+    """NaN and infinities reach the queries that see them, all of those and no others; keys that are NaN as well."""
+    torch = torch_cuda()
+    n, h, kh = 150, 4, 2
+    q, k, v = heads(torch, 1, n, h, dim), heads(torch, 2, n, kh, dim), heads(torch, 3, n, kh, dim)
+    starts = ints(torch, [0, n])
+    clean = B.attention(q, k, v, starts)
+    for at in (0, 31, 32, 70, 100, n - 1):
+        for value in (float("nan"), float("inf"), -float("inf")):
+            bad = v.clone()
+            bad[at, 1, dim - 3] = value
+            got = B.attention(q, k, bad, starts)
+            want = clean.clone()
+            want[at:, 2:, dim - 3] = value
+            assert torch.equal(torch.isnan(got), torch.isnan(want))
+            assert torch.equal(got[~torch.isnan(got)], want[~torch.isnan(want)])
+        bad = k.clone()
+        bad[at, 0, 5] = float("nan")
+        got = B.attention(q, bad, v, starts)
+        assert bool(torch.isnan(got[at:, :2]).all())
+        rest = torch.isnan(got)
+        rest[at:, :2] = False
+        assert not rest.any() and torch.equal(got[:at], clean[:at]) and torch.equal(got[:, 2:], clean[:, 2:])
+    bad = v.clone()
+    bad[40, 0, 1], bad[60, 0, 1] = float("inf"), -float("inf")
+    got = B.attention(q, k, bad, starts)[:, :2, 1]
+    assert bool(got[:40].isfinite().all()) and bool((got[40:60] == float("inf")).all()) and bool(torch.isnan(got[60:]).all())
