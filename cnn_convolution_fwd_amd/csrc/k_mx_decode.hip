@@ -33,7 +33,7 @@ using namespace mx;
 
 constexpr int kUnit = 128;      // tokens: a step of 32 for each of a workgroup's four waves
 constexpr float kLow = -3.0e38f;  // m before any score: finite, so that differences are numbers
-constexpr float kSlack = 8.0f;
+constexpr float kMost = 4096.0f;  // a lane's 8 weights sum up to this before m follows the scores
 
 struct Params {
     const uint8_t *k_codes, *k_scales, *v_codes, *v_scales;
@@ -51,117 +51,140 @@ struct Params {
     Divisor page, per_group;
 };
 
-// Sum over the lanes of a wave up to and with this one.
-__device__ __forceinline__ long long scan(long long v, int lane) {
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-        const long long o = __shfl_up(v, d);
-        if (lane >= d) v += o;
-    }
-    return v;
-}
-
 __device__ __forceinline__ int length_of(const Params& p, int seq) {
     const long long most = static_cast<long long>(p.table_pitch) * p.page_size;
     return static_cast<int>(min(static_cast<long long>(max(p.lengths[seq], 0)), most));
 }
 __device__ __forceinline__ int units_of(int length) { return max(1, (length + kUnit - 1) / kUnit); }
 
-struct Place {
-    int seq;
-    long long before;  // units of one head in the sequences before it
-};
-
-__device__ long long count_units(const Params& p, int lane) {
-    long long n = 0;
-    for (int s = lane; s < p.sequences; s += 64) n += units_of(length_of(p, s));
+// Units of one head, over all sequences: of those up to and with this lane's of the 64 from s on.
+__device__ __forceinline__ int units_upto(const Params& p, int s, int lane, int* mine) {
+    *mine = s + lane < p.sequences ? units_of(length_of(p, s + lane)) : 0;
+    int v = *mine;
 #pragma unroll
-    for (int d = 32; d; d /= 2) n += __shfl_xor(n, d);
-    return n;
+    for (int d = 1; d < 64; d *= 2) {
+        const int o = __shfl_up(v, d);
+        if (lane >= d) v += o;
+    }
+    return v;
 }
 
-// The sequence in which the x-th unit of one head lies.
-__device__ Place find_unit(const Params& p, long long x, int lane) {
-    long long before = 0;
-    for (int s = 0; s < p.sequences; s += 64) {
-        const int mine = s + lane < p.sequences ? units_of(length_of(p, s + lane)) : 0;
-        const long long upto = before + scan(mine, lane);
-        const unsigned long long past = __ballot(upto > x);
-        if (past) {
-            const int at = __ffsll(past) - 1;
-            return {s + at, __shfl(upto - mine, at)};
-        }
-        before = __shfl(upto, 63);
+// The units of all pairs (head, block of rows) of all sequences, shared out: workgroup w takes `most` or one less of them,
+// from start(w) on.
+struct Shares {
+    int units, workgroups, most, longer;  // the first `longer` workgroups take `most`
+    __device__ __forceinline__ int start(int w) const { return w * (most - 1) + min(w, longer); }
+    __device__ __forceinline__ int owner(int u) const {
+        return u < longer * most ? u / most : longer + (u - longer * most) / (most - 1);
     }
-    return {p.sequences - 1, before};
+};
+
+__device__ __forceinline__ Shares shares_of(const Params& p, int units_of_a_head) {
+    Shares r;
+    r.units = units_of_a_head * p.kv_heads * p.row_blocks;
+    r.workgroups = min(p.workgroups, r.units);
+    r.most = r.units / r.workgroups + 1;
+    r.longer = r.units - r.workgroups * (r.most - 1);
+    return r;
 }
 
 __device__ __forceinline__ f32x4 mma(const u32x4_t& a, const u32x4_t& b, const f32x4& c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
+// Two values of a block as bf16.  The scale counts with its exponent alone: the byte where a float has it, 0 meaning 2^-127
+// and 255 NaN.
 template <int SEL>
 __device__ __forceinline__ uint32_t two(uint32_t codes, float scale) {
     return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, SEL));
 }
-
-// Scale of a byte; of 255 an infinity, which with the code 0 is a NaN as well.
-__device__ __forceinline__ float unit_of(uint32_t byte) { return __uint_as_float(max(byte << 23, 0x00400000u)); }
 
 // Codes and scales of 32 tokens as a lane (n = lane % 16, g = lane / 16) needs them.
 template <int DP>
 struct Step {
     static constexpr int W = DP / 32;  // words of a token's K for each lane
     static constexpr int VW = DP >= 128 ? DP / 128 : 1;  // words of V's columns
-    uint32_t k[2][W], ks[2][DP == 256 ? 2 : 1];
-    uint32_t v[8][VW], vs[8];
+    static constexpr int SW = DP == 256 ? 2 : 1;         // words of a token's scales
+    uint32_t k[2][W], ks[2][SW];
+    uint32_t v[8][VW], vs[8][SW];
     bool there[2];  // the tile's page is one of the cache's
 };
 
+// A lane's places in a tile of 16 tokens, in bytes.  Lanes past the row's values read its last block, which meets zeros of
+// q (K) or is not stored (V).
 template <int DP>
-__device__ __forceinline__ void load_step(const Params& p, int seq, int head, int length, int token, int lane, Step<DP>& s) {
-    const int n = lane & 15, g = lane >> 4;
-    const int code_pitch = p.blocks * 16;
+struct Places {
+    uint32_t k[DP == 256 ? 2 : 1], ks[DP == 256 ? 2 : 1], v[4], vs;
+    uint32_t turn[DP == 256 ? 2 : 1];  // of a token's word of scales, to bring the byte of the lane's columns to a float's exponent
+    bool second;  // the byte is in the second word
+};
+
+template <int DP>
+__device__ __forceinline__ Places<DP> places(const Params& p, int lane) {
+    Places<DP> r;
+    const int n = lane & 15, g = lane >> 4, pitch = p.blocks * 16;
+    if constexpr (DP == 64) {
+        const int b = min(g >> 1, p.blocks - 1);
+        r.k[0] = n * pitch + b * 16 + (g & 1) * 8;
+        r.ks[0] = n * p.scale_pitch + b;
+    } else {
+#pragma unroll
+        for (int i = 0; i < DP / 128; ++i) {
+            const int b = min(g * (DP / 128) + i, p.blocks - 1);
+            r.k[i] = n * pitch + b * 16;
+            r.ks[i] = n * p.scale_pitch + b;
+        }
+    }
+    constexpr int E = DP / 16;  // values of a lane's columns
+    const int b = min(n * E / 32, p.blocks - 1);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r.v[j] = (4 * g + j) * pitch + b * 16 + n * E / 2 - n * E / 32 * 16;
+    r.vs = 4 * g * p.scale_pitch;
+    r.turn[0] = (b % 4) * 8 + 9;
+    r.second = b >= 4;
+    return r;
+}
+
+// Page of the tile of 16 tokens from t on, or -1.  All in scalar registers.
+__device__ __forceinline__ int page_of(const Params& p, int seq, int t, int length, int* offset) {
+    *offset = 0;
+    if (t >= length) return -1;
+    const int page = divide(t, p.page);
+    *offset = t - page * p.page_size;
+    typedef const __attribute__((address_space(4))) int32_t* scalar;  // read only: a scalar load
+    const int id = ((scalar)(p.table + static_cast<long long>(seq) * p.table_pitch))[page];
+    return id < p.pages ? id : -1;
+}
+
+template <int DP>
+__device__ __forceinline__ void load_step(const Params& p, const Places<DP>& at, int seq, int head, int length, int token, Step<DP>& s) {
 #pragma unroll
     for (int a = 0; a < 2; ++a) {
-        const int t = token + 16 * a;
-        int id = -1, offset = 0;
-        if (t < length) {
-            const int page = divide(t, p.page);
-            offset = t - page * p.page_size;
-            id = p.table[static_cast<long long>(seq) * p.table_pitch + page];
-        }
-        id = __builtin_amdgcn_readfirstlane(id);
-        s.there[a] = id >= 0 && id < p.pages;
-        const long long row = (static_cast<long long>(s.there[a] ? id : 0) * p.kv_heads + head) * p.page_size + offset;
-        const uint8_t* kc = p.k_codes + row * code_pitch;
-        const uint8_t* ks = p.k_scales + row * p.scale_pitch;
-        const uint8_t* vc = p.v_codes + row * code_pitch;
-        const uint8_t* vs = p.v_scales + row * p.scale_pitch;
-        // lanes past the row's values read its last block, which meets zeros of q (K) or is not stored (V)
+        int offset;
+        const int id = page_of(p, seq, token + 16 * a, length, &offset);
+        s.there[a] = id >= 0;
+        const long long row = (static_cast<long long>(max(id, 0)) * p.kv_heads + head) * p.page_size + offset;
+        const uint8_t *kc = p.k_codes + row * (p.blocks * 16), *ks = p.k_scales + row * p.scale_pitch;
+        const uint8_t *vc = p.v_codes + row * (p.blocks * 16), *vs = p.v_scales + row * p.scale_pitch;
         if constexpr (DP == 64) {
-            const int b = min(g >> 1, p.blocks - 1);
-            const uint2 w = *reinterpret_cast<const uint2*>(kc + n * code_pitch + b * 16 + (g & 1) * 8);
+            const uint2 w = *reinterpret_cast<const uint2*>(kc + at.k[0]);
             s.k[a][0] = w.x;
             s.k[a][1] = w.y;
-            s.ks[a][0] = ks[n * p.scale_pitch + b];
+            s.ks[a][0] = ks[at.ks[0]];
         } else {
 #pragma unroll
             for (int i = 0; i < DP / 128; ++i) {
-                const int b = min(g * (DP / 128) + i, p.blocks - 1);
-                const uint4 w = *reinterpret_cast<const uint4*>(kc + n * code_pitch + b * 16);
+                const uint4 w = *reinterpret_cast<const uint4*>(kc + at.k[i]);
                 s.k[a][4 * i] = w.x;
                 s.k[a][4 * i + 1] = w.y;
                 s.k[a][4 * i + 2] = w.z;
                 s.k[a][4 * i + 3] = w.w;
-                s.ks[a][i] = ks[n * p.scale_pitch + b];
+                s.ks[a][i] = ks[at.ks[i]];
             }
         }
-        constexpr int E = DP / 16;  // values of a lane's columns
-        const int b = min(n * E / 32, p.blocks - 1), in = n * E / 2 - n * E / 32 * 16;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const uint8_t* c = vc + (4 * g + j) * code_pitch + b * 16 + in;
+            const uint8_t* c = vc + at.v[j];
             if constexpr (DP == 64) s.v[4 * a + j][0] = *reinterpret_cast<const uint16_t*>(c);
             if constexpr (DP == 128) s.v[4 * a + j][0] = *reinterpret_cast<const uint32_t*>(c);
             if constexpr (DP == 256) {
@@ -169,7 +192,22 @@ __device__ __forceinline__ void load_step(const Params& p, int seq, int head, in
                 s.v[4 * a + j][0] = w.x;
                 s.v[4 * a + j][1] = w.y;
             }
-            s.vs[4 * a + j] = vs[(4 * g + j) * p.scale_pitch + b];
+        }
+        // four tokens' words of scales lie side by side, of which a lane uses one byte each
+        if constexpr (DP == 256) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t* w = reinterpret_cast<const uint32_t*>(vs + at.vs + j * p.scale_pitch);
+                s.vs[4 * a + j][0] = w[0];
+                s.vs[4 * a + j][1] = w[1];
+            }
+        } else {
+            struct __attribute__((aligned(4))) Four {
+                uint32_t w[4];
+            };
+            const Four w = *reinterpret_cast<const Four*>(vs + at.vs);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s.vs[4 * a + j][0] = w.w[j];
         }
     }
 }
@@ -183,9 +221,9 @@ struct State {
 };
 
 template <int DP, int RT>
-__device__ __forceinline__ void attend(const Params& p, const Step<DP>& s, int seq, int head, int token, int length,
-                                       const int (&seen)[RT], int least, const u32x4_t (&q)[RT][DP / 32], int lane,
-                                       State<DP, RT>& st) {
+__device__ __forceinline__ void attend(const Params& p, const Places<DP>& at, const Step<DP>& s, int seq, int head, int token,
+                                       int length, const int (&seen)[RT], int least, const u32x4_t (&q)[RT][DP / 32],
+                                       int lane, State<DP, RT>& st) {
     constexpr int E = DP / 16, W = DP / 32;
     const int g = lane >> 4;
     f32x4 score[RT][2];
@@ -195,23 +233,26 @@ __device__ __forceinline__ void attend(const Params& p, const Step<DP>& s, int s
         for (int r = 0; r < RT; ++r) score[r][a] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int c = 0; c < W; ++c) {
-            const float unit = unit_of(s.ks[a][c / 4]);
+            const float unit = __uint_as_float(s.ks[a][c / 4] << 23);
             const uint32_t w = s.k[a][c];
             const u32x4_t f = {two<0>(w, unit), two<1>(w, unit), two<2>(w, unit), two<3>(w, unit)};
 #pragma unroll
             for (int r = 0; r < RT; ++r) score[r][a] = mma(f, q[r][c], score[r][a]);
         }
     }
-    uint32_t vs[8], v[8][Step<DP>::VW];
+    uint32_t v[8][Step<DP>::VW];
+    float unit[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        vs[j] = s.vs[j];
+        const uint32_t w = DP == 256 && at.second ? s.vs[j][Step<DP>::SW - 1] : s.vs[j][0];
+        unit[j] = __uint_as_float(__builtin_amdgcn_alignbit(w, w, at.turn[0]) & 0x7f800000u);
 #pragma unroll
         for (int w = 0; w < Step<DP>::VW; ++w) v[j][w] = s.v[j][w];
     }
     bool odd = false;  // a value that is NaN, of a token that not all queries may see
     const bool masked = token + 32 > least || !s.there[0] || !s.there[1];
     if (masked) {
+        asm volatile("");  // a branch around this stays one
 #pragma unroll
         for (int a = 0; a < 2; ++a)
 #pragma unroll
@@ -221,10 +262,10 @@ __device__ __forceinline__ void attend(const Params& p, const Step<DP>& s, int s
                 for (int r = 0; r < RT; ++r)
                     if (!s.there[a] || t >= seen[r]) score[r][a][j] = -__builtin_inff();
                 // weights of 0 do not undo a NaN: it is taken out, and put back below where it is seen
-                const bool absent = !s.there[a] || t >= length;
-                odd |= !absent && vs[4 * a + j] == 255;
-                if (absent || vs[4 * a + j] == 255) {
-                    vs[4 * a + j] = 127;
+                const bool absent = !s.there[a] || t >= length, nan = unit[4 * a + j] == __builtin_inff();
+                odd |= !absent && nan;
+                if (absent || nan) {
+                    unit[4 * a + j] = 1.0f;
 #pragma unroll
                     for (int w = 0; w < Step<DP>::VW; ++w) v[4 * a + j][w] = 0;
                 }
@@ -233,39 +274,51 @@ __device__ __forceinline__ void attend(const Params& p, const Step<DP>& s, int s
     u32x4_t weight[RT];
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
-        float top = score[r][0][0];
+        float sum = 0.0f;
+        auto weigh = [&]() __attribute__((always_inline)) {
+            sum = 0.0f;
+            float e[8];
 #pragma unroll
-        for (int i = 1; i < 8; ++i) top = fmaxf(top, score[r][i / 4][i % 4]);
-        top *= p.scale2;
-        if (__any(top > st.m[r] + kSlack)) {
+            for (int i = 0; i < 8; ++i)
+                e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(score[r][i / 4][i % 4], p.scale2, -st.m[r]));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                weight[r][i] = pack_bf16x2(e[2 * i], e[2 * i + 1]);
+                // the sum takes the weights as they enter the product: rounded
+                sum = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2_t, static_cast<uint32_t>(weight[r][i])),
+                                                      __builtin_bit_cast(bf16x2_t, 0x3f803f80u), sum, false);
+            }
+        };
+        weigh();
+        if (__any(!(sum <= kMost))) {
+            // scores far above m (or the first ones, or NaN): m moves up to the query's largest, and the weights are taken again
+            float top = score[r][0][0];
+#pragma unroll
+            for (int i = 1; i < 8; ++i) top = fmaxf(top, score[r][i / 4][i % 4]);
             top = fmaxf(top, __shfl_xor(top, 16));
-            top = fmaxf(top, __shfl_xor(top, 32));
-            const float m = top > st.m[r] + kSlack ? top : st.m[r], f = __builtin_amdgcn_exp2f(st.m[r] - m);
+            top = fmaxf(top, __shfl_xor(top, 32)) * p.scale2;
+            int over = !(sum <= kMost);
+            over |= __shfl_xor(over, 16);
+            over |= __shfl_xor(over, 32);
+            const float m = over && top > st.m[r] ? top : st.m[r], f = __builtin_amdgcn_exp2f(st.m[r] - m);
             st.m[r] = m;
             st.l[r] *= f;
 #pragma unroll
             for (int i = 0; i < E; ++i) st.o[r][i] *= f;
+            weigh();
         }
-        float e[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(score[r][i / 4][i % 4], p.scale2, -st.m[r]));
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            weight[r][i] = pack_bf16x2(e[2 * i], e[2 * i + 1]);
-            // the sum takes the weights as they enter the product: rounded
-            st.l[r] = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2_t, static_cast<uint32_t>(weight[r][i])),
-                                                      __builtin_bit_cast(bf16x2_t, 0x3f803f80u), st.l[r], false);
-        }
+        st.l[r] += sum;
     }
 #pragma unroll
     for (int b = 0; b < E / 2; ++b) {  // byte b of the columns: values 2 b and 2 b + 1
         uint32_t x[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const float unit = unit_of(vs[j]);
             const uint32_t w = v[j][b / 4];
-            x[j] = b % 4 == 0 ? two<0>(w, unit) : b % 4 == 1 ? two<1>(w, unit) : b % 4 == 2 ? two<2>(w, unit) : two<3>(w, unit);
+            x[j] = b % 4 == 0   ? two<0>(w, unit[j])
+                   : b % 4 == 1 ? two<1>(w, unit[j])
+                   : b % 4 == 2 ? two<2>(w, unit[j])
+                                : two<3>(w, unit[j]);
         }
         u32x4_t even, uneven;
 #pragma unroll
@@ -309,21 +362,39 @@ __global__ __launch_bounds__(256, DP * RT <= 128 ? 3 : DP * RT <= 256 ? 2 : 1) v
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 15, g = lane >> 4;
     const int pairs = p.kv_heads * p.row_blocks;  // of a sequence: (head, block of rows)
-    const long long units = count_units(p, lane) * pairs;
-    const long long workgroups = min(static_cast<long long>(p.workgroups), units);
-    if (static_cast<long long>(blockIdx.x) >= workgroups) return;
-    long long u = blockIdx.x * units / workgroups;
-    const long long end = (blockIdx.x + 1) * units / workgroups;
-    Place at = find_unit(p, u / pairs, lane);
-    int seq = __builtin_amdgcn_readfirstlane(at.seq);
+    // the units of all sequences, then the sequence in which the first unit of this workgroup lies
+    int mine, upto = units_upto(p, 0, lane, &mine), total = __shfl(upto, 63);
+    for (int s = 64; s < p.sequences; s += 64) total += __shfl(units_upto(p, s, lane, &mine), 63);
+    const Shares shares = shares_of(p, __builtin_amdgcn_readfirstlane(total));
+    if (static_cast<int>(blockIdx.x) >= shares.workgroups) return;
+    int u = shares.start(blockIdx.x);
+    const int end = shares.start(blockIdx.x + 1);
+    int seq = 0, before = 0;
+    {
+        const int x = u / pairs;
+        if (p.sequences > 64) upto = units_upto(p, 0, lane, &mine);
+        for (int s = 0; s < p.sequences; s += 64) {
+            const unsigned long long past = __ballot(before + upto > x);
+            if (past) {
+                const int at = __ffsll(past) - 1;
+                seq = s + at;
+                before += __shfl(upto - mine, at);
+                break;
+            }
+            before += __shfl(upto, 63);
+            upto = units_upto(p, s + 64, lane, &mine);
+        }
+    }
+    seq = __builtin_amdgcn_readfirstlane(seq);
     int length = __builtin_amdgcn_readfirstlane(length_of(p, seq));
-    long long in_seq = u - at.before * pairs;
-    int pair = __builtin_amdgcn_readfirstlane(static_cast<int>(in_seq / units_of(length)));
-    int first = __builtin_amdgcn_readfirstlane(static_cast<int>(in_seq - static_cast<long long>(pair) * units_of(length)));
+    const int in_seq = __builtin_amdgcn_readfirstlane(u - before * pairs);
+    int pair = min(__builtin_amdgcn_readfirstlane(in_seq / units_of(length)), pairs - 1);
+    int first = __builtin_amdgcn_readfirstlane(in_seq - pair * units_of(length));
+    const Places<DP> at = places<DP>(p, lane);
     int slot = 2 * blockIdx.x;
     while (u < end) {
         const int all = units_of(length);
-        const int count = __builtin_amdgcn_readfirstlane(static_cast<int>(min(static_cast<long long>(all - first), end - u)));
+        const int count = __builtin_amdgcn_readfirstlane(min(all - first, end - u));
         const int head = pair / p.row_blocks, row0 = (pair - head * p.row_blocks) * p.row_block;
         const int stop = min((first + count) * kUnit, length);
         State<DP, RT> st;
@@ -346,14 +417,18 @@ __global__ __launch_bounds__(256, DP * RT <= 128 ? 3 : DP * RT <= 256 ? 2 : 1) v
 #pragma unroll
             for (int i = 0; i < E; ++i) st.o[r][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         }
-        int token = first * kUnit + wave * 32;
-        if (token < stop) {
-            Step<DP> now, next;
-            load_step<DP>(p, seq, head, length, token, lane, now);
-            for (; token < stop; token += kUnit) {
-                load_step<DP>(p, seq, head, length, token + kUnit < stop ? token + kUnit : length, lane, next);
-                attend<DP, RT>(p, now, seq, head, token, length, seen, least, q, lane, st);
-                now = next;
+        {
+            // two steps' codes in turn: while one is used, the other is on its way
+            Step<DP> even, uneven;
+            int token = first * kUnit + wave * 32;
+            load_step<DP>(p, at, seq, head, token < stop ? length : 0, token, even);
+            load_step<DP>(p, at, seq, head, token + kUnit < stop ? length : 0, token + kUnit, uneven);
+            for (; token < stop; token += 2 * kUnit) {
+                attend<DP, RT>(p, at, even, seq, head, token, length, seen, least, q, lane, st);
+                load_step<DP>(p, at, seq, head, token + 2 * kUnit < stop ? length : 0, token + 2 * kUnit, even);
+                if (token + kUnit >= stop) break;
+                attend<DP, RT>(p, at, uneven, seq, head, token + kUnit, length, seen, least, q, lane, st);
+                load_step<DP>(p, at, seq, head, token + 3 * kUnit < stop ? length : 0, token + 3 * kUnit, uneven);
             }
         }
         // join the four waves: m first, then the sums, 2 and 3 into 0 and 1, 1 into 0
@@ -436,7 +511,8 @@ __global__ __launch_bounds__(256, DP * RT <= 128 ? 3 : DP * RT <= 256 ? 2 : 1) v
         first = 0;
         if (++pair == pairs && u < end) {
             pair = 0;
-            length = __builtin_amdgcn_readfirstlane(length_of(p, ++seq));
+            seq = min(seq + 1, p.sequences - 1);
+            length = __builtin_amdgcn_readfirstlane(length_of(p, seq));
         }
     }
 }
@@ -451,7 +527,7 @@ __global__ __launch_bounds__(256) void join_kernel(Params p) {
     if (row >= p.rows) return;
     const int mine = units_of(length_of(p, seq));
     if (mine == 1) return;
-    long long n = 0, before = 0;
+    int n = 0, before = 0;
     for (int s = lane; s < p.sequences; s += 64) {
         const int c = units_of(length_of(p, s));
         n += c;
@@ -462,14 +538,11 @@ __global__ __launch_bounds__(256) void join_kernel(Params p) {
         n += __shfl_xor(n, d);
         before += __shfl_xor(before, d);
     }
-    const long long units = n * pairs, workgroups = min(static_cast<long long>(p.workgroups), units);
-    const long long u0 = before * pairs + static_cast<long long>(pair) * mine;
-    // workgroup w takes the units from w * units / workgroups on
-    const int w0 = static_cast<int>(((u0 + 1) * workgroups - 1) / units);
-    const int w1 = static_cast<int>(((u0 + mine) * workgroups - 1) / units);
+    const Shares shares = shares_of(p, n);
+    const int u0 = before * pairs + pair * mine, w0 = shares.owner(u0), w1 = shares.owner(u0 + mine - 1);
     if (w0 == w1) return;
     auto place = [&](int w) {
-        const int slot = 2 * w + (w * units / workgroups >= u0 ? 0 : 1);
+        const int slot = 2 * w + (shares.start(w) >= u0 ? 0 : 1);
         return static_cast<long long>(slot) * p.row_block + in_block;
     };
     float m = kLow;
