@@ -25,6 +25,7 @@ cfwd_status attention(const cfwd_attention_desc* d, const void* q, const void* k
 
 #if defined(__HIPCC__)
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+typedef int i32x8_t __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 #endif
 

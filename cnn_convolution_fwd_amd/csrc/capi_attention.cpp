@@ -107,11 +107,13 @@ cfwd_status check_cache_attention(const cfwd_mx_cache_attention_desc* d, const c
     if (c->head_dim % 32 || c->head_dim > 256)
         return set_error(CFWD_ERR_UNSUPPORTED, "attention over the cache needs a head_dim that is a multiple of 32, at most 256");
     if (c->page_size % 16) return set_error(CFWD_ERR_UNSUPPORTED, "attention over the cache needs a page_size that is a multiple of 16");
+    if (static_cast<long long>(c->page_size) * c->kv_heads * mx_code_pitch(c->head_dim) >= (1ll << 31))
+        return set_error(CFWD_ERR_UNSUPPORTED, "attention over the cache needs pages of fewer than 2^31 bytes of codes");
     if (d->tokens > 1024) return set_error(CFWD_ERR_UNSUPPORTED, "attention over the cache takes at most 1024 tokens a sequence");
     if (static_cast<long long>(d->sequences) * d->q_heads * std::max(d->tokens, 1) >= (1ll << 31) / 16)
         return set_error(CFWD_ERR_UNSUPPORTED, "too many queries for one call");
-    // units of work are counted in 32 bits: 128 tokens of a head for 16 queries at least
-    const long long units = (static_cast<long long>(d->table_pitch) * c->page_size + 127) / 128 * c->kv_heads *
+    // units of work are counted in 32 bits: 128 tokens of a head for 16 queries at least, and some for each pair of these
+    const long long units = (static_cast<long long>(d->table_pitch) * c->page_size / 128 + 8) * c->kv_heads *
                             ((static_cast<long long>(d->tokens) * (d->q_heads / c->kv_heads) + 15) / 16);
     if (d->sequences > 0 && units >= (1ll << 31) / d->sequences)
         return set_error(CFWD_ERR_UNSUPPORTED, "the page table stands for too many tokens for one call");

@@ -6,15 +6,23 @@
 // a group; 16 of them are one side of the matrix instruction, so that a head's
 // cache is read once for all.  S^T = K q^T has a query in each lane's column and
 // four keys in its registers, which is how P^T enters O^T = V^T P^T: nothing
-// moves between lanes.  With m the running maximum and l the running sum,
-// O and l are multiplied by 2^(m - m') only where a score passes m by more than
-// 2^8: until then weights up to 2^8 are as good.  A row goes by its own scores
-// alone, so that its result does not depend on the others'.
+// moves between lanes.
 //
-// One wave works on 32 tokens at a time.  The codes go from memory to registers:
-// of K, a lane holds whole runs of one token's values; of V, the same columns of
-// eight tokens, which after conversion (exact: a code has two significant bits)
-// are paired token by token.
+// K goes into the matrix cores as it lies in the cache, codes and scale bytes; the
+// queries beside it are two parts of 8 bits (Queries).  V's scales belong to
+// tokens, over which the second product sums, so its codes become bf16 (exact: a
+// code has two significant bits) and are paired token by token.
+//
+// Softmax.  Weights are 2^(s - m) with s in units of log2 and m no running maximum
+// but any number that the scores have not passed by far: it moves only where a
+// lane's 8 weights sum up to more than 2^12, then to the query's largest score, and
+// O and l are multiplied by 2^(m - m').  Weights have bf16's 8 bits at any size, so
+// nothing is lost.  A row goes by its own scores alone.
+//
+// One wave works on 32 tokens at a time, out of registers, while the codes of the
+// next two such steps are on their way to its own part of LDS, by copies that
+// bypass the registers: with the codes on their way to registers instead, only three
+// workgroups fit a CU instead of four.
 //
 // Work is split by the lengths, which only the device knows: a unit is 128
 // tokens of one sequence and head, every workgroup counts all units and takes an
@@ -25,6 +33,7 @@
 #include "mx.h"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace cfwd {
 namespace decode {
@@ -32,8 +41,12 @@ namespace decode {
 using namespace mx;
 
 constexpr int kUnit = 128;      // tokens: a step of 32 for each of a workgroup's four waves
+constexpr int kStart = 3;
 constexpr float kLow = -3.0e38f;  // m before any score: finite, so that differences are numbers
 constexpr float kMost = 4096.0f;  // a lane's 8 weights sum up to this before m follows the scores
+
+// Workgroups on a CU: what registers (and LDS) allow without spilling, for heads of dp values and rt * 16 queries at once.
+constexpr int resident(int dp, int rt) { return dp * rt > 256 ? 1 : dp * rt > 128 ? 2 : rt == 1 ? 4 : 3; }
 
 struct Params {
     const uint8_t *k_codes, *k_scales, *v_codes, *v_scales;
@@ -44,6 +57,7 @@ struct Params {
     int sequences, tokens, heads, kv_heads, group, dim;
     int pages, page_size, table_pitch;
     int blocks, scale_pitch;  // of a row: code blocks, bytes of scales
+    uint32_t page_codes, page_scales;  // bytes of a page
     int rows, row_blocks, row_block;  // queries of a cache's head, in blocks of row_block
     int workgroups;
     float scale2;  // scale * log2(e)
@@ -70,10 +84,11 @@ __device__ __forceinline__ int units_upto(const Params& p, int s, int lane, int*
 }
 
 // The units of all pairs (head, block of rows) of all sequences, shared out: workgroup w takes `most` or one less of them,
-// from start(w) on.
+// from begin(w) on.  To begin a pair and to write its sums takes as long as several units of its tokens do, so where a
+// workgroup has many, a pair counts as `start` units more, ahead of its own (64 sequences of up to 8192 tokens: the last workgroup ends after 68 us without, 54 with 3).
 struct Shares {
-    int units, workgroups, most, longer;  // the first `longer` workgroups take `most`
-    __device__ __forceinline__ int start(int w) const { return w * (most - 1) + min(w, longer); }
+    int units, workgroups, most, longer, start;  // the first `longer` workgroups take `most`
+    __device__ __forceinline__ int begin(int w) const { return w * (most - 1) + min(w, longer); }
     __device__ __forceinline__ int owner(int u) const {
         return u < longer * most ? u / most : longer + (u - longer * most) / (most - 1);
     }
@@ -81,7 +96,9 @@ struct Shares {
 
 __device__ __forceinline__ Shares shares_of(const Params& p, int units_of_a_head) {
     Shares r;
-    r.units = units_of_a_head * p.kv_heads * p.row_blocks;
+    const int pairs = p.kv_heads * p.row_blocks;
+    r.start = units_of_a_head * pairs >= 4 * p.workgroups ? kStart : 0;
+    r.units = (units_of_a_head + r.start * p.sequences) * pairs;
     r.workgroups = min(p.workgroups, r.units);
     r.most = r.units / r.workgroups + 1;
     r.longer = r.units - r.workgroups * (r.most - 1);
@@ -102,114 +119,247 @@ __device__ __forceinline__ uint32_t two(uint32_t codes, float scale) {
 // Codes and scales of 32 tokens as a lane (n = lane % 16, g = lane / 16) needs them.
 template <int DP>
 struct Step {
-    static constexpr int W = DP / 32;  // words of a token's K for each lane
+    static constexpr int KB = DP == 256 ? 2 : 1;         // blocks of a token's K for each lane: 4 i + g
     static constexpr int VW = DP >= 128 ? DP / 128 : 1;  // words of V's columns
     static constexpr int SW = DP == 256 ? 2 : 1;         // words of a token's scales
-    uint32_t k[2][W], ks[2][SW];
+    u32x4_t k[2][KB];
+    uint32_t ks[2][KB];
     uint32_t v[8][VW], vs[8][SW];
-    bool there[2];  // the tile's page is one of the cache's
 };
 
 // A lane's places in a tile of 16 tokens, in bytes.  Lanes past the row's values read its last block, which meets zeros of
 // q (K) or is not stored (V).
 template <int DP>
 struct Places {
-    uint32_t k[DP == 256 ? 2 : 1], ks[DP == 256 ? 2 : 1], v[4], vs;
-    uint32_t turn[DP == 256 ? 2 : 1];  // of a token's word of scales, to bring the byte of the lane's columns to a float's exponent
+    uint32_t k[Step<DP>::KB], ks[Step<DP>::KB], v[4], vs;
+    uint32_t turn;  // of a token's word of scales, to bring the byte of the lane's columns to a float's exponent
     bool second;  // the byte is in the second word
 };
 
+// To another stage.  Opaque, so that the reads hold what their own places differ by.
 template <int DP>
-__device__ __forceinline__ Places<DP> places(const Params& p, int lane) {
+__device__ __forceinline__ void move(Places<DP>& r, uint32_t by) {
+#pragma unroll
+    for (int i = 0; i < Step<DP>::KB; ++i) asm volatile("" : "+v"(r.k[i] += by), "+v"(r.ks[i] += by));
+#pragma unroll
+    for (int j = 0; j < 4; ++j) asm volatile("" : "+v"(r.v[j] += by));
+    asm volatile("" : "+v"(r.vs += by));
+}
+
+template <int DP>
+__device__ __forceinline__ Places<DP> places(const Params& p, int lane, uint32_t lds) {
     Places<DP> r;
     const int n = lane & 15, g = lane >> 4, pitch = p.blocks * 16;
-    if constexpr (DP == 64) {
-        const int b = min(g >> 1, p.blocks - 1);
-        r.k[0] = n * pitch + b * 16 + (g & 1) * 8;
-        r.ks[0] = n * p.scale_pitch + b;
-    } else {
 #pragma unroll
-        for (int i = 0; i < DP / 128; ++i) {
-            const int b = min(g * (DP / 128) + i, p.blocks - 1);
-            r.k[i] = n * pitch + b * 16;
-            r.ks[i] = n * p.scale_pitch + b;
-        }
+    for (int i = 0; i < Step<DP>::KB; ++i) {
+        const int b = min(4 * i + g, p.blocks - 1);
+        r.k[i] = n * pitch + b * 16;
+        r.ks[i] = n * p.scale_pitch + b;
     }
     constexpr int E = DP / 16;  // values of a lane's columns
     const int b = min(n * E / 32, p.blocks - 1);
 #pragma unroll
     for (int j = 0; j < 4; ++j) r.v[j] = (4 * g + j) * pitch + b * 16 + n * E / 2 - n * E / 32 * 16;
     r.vs = 4 * g * p.scale_pitch;
-    r.turn[0] = (b % 4) * 8 + 9;
+    r.turn = (b % 4) * 8 + 9;
     r.second = b >= 4;
+    move(r, lds);
     return r;
 }
 
-// Page of the tile of 16 tokens from t on, or -1.  All in scalar registers.
-__device__ __forceinline__ int page_of(const Params& p, int seq, int t, int length, int* offset) {
-    *offset = 0;
-    if (t >= length) return -1;
-    const int page = divide(t, p.page);
-    *offset = t - page * p.page_size;
-    typedef const __attribute__((address_space(4))) int32_t* scalar;  // read only: a scalar load
-    const int id = ((scalar)(p.table + static_cast<long long>(seq) * p.table_pitch))[page];
-    return id < p.pages ? id : -1;
+// Where the two tiles of 16 tokens of a step lie, in bytes of codes and scales, and whether their pages are the cache's.  All in
+// scalar registers.  ONE: pages are whole steps, so that the tiles lie one behind the other.
+template <bool ONE>
+struct Where {
+    static constexpr int N = ONE ? 1 : 2;
+    uint64_t codes[N], scales[N];
+    bool there[N];
+    __device__ __forceinline__ bool has(int a) const { return there[ONE ? 0 : a]; }
+};
+
+template <bool ONE>
+__device__ __forceinline__ Where<ONE> where_is(const Params& p, const int32_t* pages_of, int head, int token, int length) {
+    Where<ONE> r;
+#pragma unroll
+    for (int a = 0; a < Where<ONE>::N; ++a) {
+        const int t = token + 16 * a;
+        int row = head * p.page_size, id = -1;
+        if (t < length) {
+            const int page = divide(t, p.page);
+            row += t - page * p.page_size;
+            typedef const __attribute__((address_space(4))) int32_t* scalar;  // read only: a scalar load
+            id = ((scalar)pages_of)[page];
+        }
+        r.there[a] = static_cast<uint32_t>(id) < static_cast<uint32_t>(p.pages);
+        const uint32_t of = r.there[a] ? id : 0;
+        r.codes[a] = static_cast<uint64_t>(of) * p.page_codes + static_cast<uint32_t>(row * p.blocks * 16);
+        r.scales[a] = static_cast<uint64_t>(of) * p.page_scales + static_cast<uint32_t>(row * p.scale_pitch);
+    }
+    return r;
 }
 
+// A step in LDS: the tiles' codes of K, of V, their scales; each wave has kStages of them, and waits for nobody.
 template <int DP>
-__device__ __forceinline__ void load_step(const Params& p, const Places<DP>& at, int seq, int head, int length, int token, Step<DP>& s) {
+constexpr int kTile = DP * 8;  // bytes of 16 tokens' codes
+template <int DP>
+constexpr int kScales = DP == 256 ? 128 : 64;
+template <int DP>
+constexpr int kStage = 4 * kTile<DP> + 4 * kScales<DP>;
+constexpr int kStages = 2;
+template <int DP, bool ONE>
+constexpr int kCopies = 4 * (DP == 256 ? 2 : 1) + (ONE ? 2 : 4);  // memory instructions of a step
+
+// Copies a lane's 16 (or 4) bytes from a buffer straight to LDS, lane after lane from `lds` on (the same for the wave).  The
+// compiler does not see these loads: wait_loads() comes before the data are read.  It may have moved the buffer's words to
+// scalar registers with vector instructions, which a load must not follow closer than five wait states.
+__device__ __forceinline__ void load_to_lds16(const __amdgpu_buffer_rsrc_t& b, uint32_t off, uint32_t lds) {
+    asm volatile("s_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" : : "{m0}"(lds), "v"(off), "s"(b) : "memory");
+}
+__device__ __forceinline__ void load_to_lds4(const __amdgpu_buffer_rsrc_t& b, uint32_t off, uint32_t lds) {
+    asm volatile("s_nop 4\n\tbuffer_load_dword %1, %2, 0 offen lds" : : "{m0}"(lds), "v"(off), "s"(b) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void wait_loads() {  // until at most N of this wave's loads are outstanding
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+// All waves of the workgroup, each with what it wrote to LDS there; stores to memory go on.
+__device__ __forceinline__ void barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+// Bytes from a scalar address on; beyond them a copy writes zeros.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const uint8_t* base, uint64_t at, int bytes) {
+    const uint64_t a = reinterpret_cast<uint64_t>(base) + at;
+    const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(a));
+    const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(a >> 32));
+    return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(static_cast<uint64_t>(hi) << 32 | lo), 0,
+                                             __builtin_amdgcn_readfirstlane(bytes), 0x00020000);
+}
+
+template <int DP, bool ONE>
+__device__ __forceinline__ void copy_step(const Params& p, const Where<ONE>& where, int lane, uint32_t to) {
+    const int tile = p.blocks * 256, tile_scales = p.scale_pitch * 16;  // bytes
+#pragma unroll
+    for (int w = 0; w < Where<ONE>::N; ++w) {
+        const auto kc = buffer(p.k_codes, where.codes[w], ONE ? 2 * tile : tile);
+        const auto vc = buffer(p.v_codes, where.codes[w], ONE ? 2 * tile : tile);
+#pragma unroll
+        for (int a = w; a < (ONE ? 2 : w + 1); ++a)
+#pragma unroll
+            for (int i = 0; i < (DP == 256 ? 2 : 1); ++i)
+                if (DP >= 128 || lane < 32) {  // what lies past the tile's rows is not read
+                    const uint32_t off = (ONE ? a * tile : 0) + lane * 16 + i * 1024;
+                    load_to_lds16(kc, off, to + a * kTile<DP> + i * 1024);
+                    load_to_lds16(vc, off, to + (2 + a) * kTile<DP> + i * 1024);
+                }
+        const auto ks = buffer(p.k_scales, where.scales[w], ONE ? 2 * tile_scales : tile_scales);
+        const auto vs = buffer(p.v_scales, where.scales[w], ONE ? 2 * tile_scales : tile_scales);
+        if (lane < kScales<DP> / 4 * (ONE ? 2 : 1)) {
+            load_to_lds4(ks, lane * 4, to + 4 * kTile<DP> + w * kScales<DP>);
+            load_to_lds4(vs, lane * 4, to + 4 * kTile<DP> + (2 + w) * kScales<DP>);
+        }
+    }
+}
+
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+template <typename T>
+__device__ __forceinline__ T lds_at(uint32_t at) {
+    return *reinterpret_cast<const __attribute__((address_space(3))) T*>(at);
+}
+
+// A lane's places are addresses in LDS, and the reads hold the rest.
+template <int DP>
+__device__ __forceinline__ void read_step(const Places<DP>& at, Step<DP>& s) {
 #pragma unroll
     for (int a = 0; a < 2; ++a) {
-        int offset;
-        const int id = page_of(p, seq, token + 16 * a, length, &offset);
-        s.there[a] = id >= 0;
-        const long long row = (static_cast<long long>(max(id, 0)) * p.kv_heads + head) * p.page_size + offset;
-        const uint8_t *kc = p.k_codes + row * (p.blocks * 16), *ks = p.k_scales + row * p.scale_pitch;
-        const uint8_t *vc = p.v_codes + row * (p.blocks * 16), *vs = p.v_scales + row * p.scale_pitch;
-        if constexpr (DP == 64) {
-            const uint2 w = *reinterpret_cast<const uint2*>(kc + at.k[0]);
-            s.k[a][0] = w.x;
-            s.k[a][1] = w.y;
-            s.ks[a][0] = ks[at.ks[0]];
-        } else {
+        constexpr int SCALES = 4 * kTile<DP>;
+        const int kc = a * kTile<DP>, vc = kc + 2 * kTile<DP>, ks = SCALES + a * kScales<DP>, vs = ks + 2 * kScales<DP>;
 #pragma unroll
-            for (int i = 0; i < DP / 128; ++i) {
-                const uint4 w = *reinterpret_cast<const uint4*>(kc + at.k[i]);
-                s.k[a][4 * i] = w.x;
-                s.k[a][4 * i + 1] = w.y;
-                s.k[a][4 * i + 2] = w.z;
-                s.k[a][4 * i + 3] = w.w;
-                s.ks[a][i] = ks[at.ks[i]];
-            }
+        for (int i = 0; i < Step<DP>::KB; ++i) {
+            s.k[a][i] = lds_at<u32x4_t>(kc + at.k[i]);
+            s.ks[a][i] = lds_at<uint8_t>(ks + at.ks[i]);
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const uint8_t* c = vc + at.v[j];
-            if constexpr (DP == 64) s.v[4 * a + j][0] = *reinterpret_cast<const uint16_t*>(c);
-            if constexpr (DP == 128) s.v[4 * a + j][0] = *reinterpret_cast<const uint32_t*>(c);
+            if constexpr (DP == 64) s.v[4 * a + j][0] = lds_at<uint16_t>(vc + at.v[j]);
+            if constexpr (DP == 128) s.v[4 * a + j][0] = lds_at<uint32_t>(vc + at.v[j]);
             if constexpr (DP == 256) {
-                const uint2 w = *reinterpret_cast<const uint2*>(c);
-                s.v[4 * a + j][0] = w.x;
-                s.v[4 * a + j][1] = w.y;
+                const auto w = lds_at<u32x2_t>(vc + at.v[j]);
+                s.v[4 * a + j][0] = w[0];
+                s.v[4 * a + j][1] = w[1];
             }
         }
         // four tokens' words of scales lie side by side, of which a lane uses one byte each
-        if constexpr (DP == 256) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint32_t* w = reinterpret_cast<const uint32_t*>(vs + at.vs + j * p.scale_pitch);
-                s.vs[4 * a + j][0] = w[0];
-                s.vs[4 * a + j][1] = w[1];
-            }
-        } else {
-            struct __attribute__((aligned(4))) Four {
-                uint32_t w[4];
-            };
-            const Four w = *reinterpret_cast<const Four*>(vs + at.vs);
+        for (int i = 0; i < Step<DP>::SW; ++i) {
+            const auto w = lds_at<u32x4_t>(vs + at.vs + 16 * i);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) s.vs[4 * a + j][0] = w.w[j];
+            for (int j = 0; j < 4; ++j) s.vs[4 * a + (4 * i + j) / Step<DP>::SW][j % Step<DP>::SW] = w[j];
         }
     }
+}
+
+// 16 queries as the matrix instruction takes them beside codes of 4 bits: in two parts of 8 bits (e4m3), hi + lo / 16, of
+// values with a common scale that brings the largest, of a query's 128, into [2^7, 2^8).  A bf16 has eight significant bits and
+// an e4m3 four, of which the second part needs as many as the rounding of the first leaves: the sum is exact for
+// values down to 2^-13 of the largest, and within 2^-21 of the largest below.  Lane (n, g) holds values 16 g .. 16 g + 15 and
+// 64 on of query n.
+template <int DP>
+struct Queries {
+    static constexpr int KB = Step<DP>::KB;
+    i32x8_t hi[KB], lo[KB];
+    int scale[KB];
+};
+
+template <int DP>
+__device__ __forceinline__ void load_queries(const Params& p, const bf16_t* x, int g, Queries<DP>& q) {
+#pragma unroll
+    for (int i = 0; i < Queries<DP>::KB; ++i) {
+        float v[32];
+        uint32_t top = 0;
+#pragma unroll
+        for (int j = 0; j < 32; j += 8) {
+            const int d = 128 * i + 64 * (j / 16) + 16 * g + j % 16;
+            const u32x4_t w = d < p.dim ? *reinterpret_cast<const u32x4_t*>(x + d) : u32x4_t{0, 0, 0, 0};
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                v[j + 2 * c] = __uint_as_float(w[c] << 16);
+                v[j + 2 * c + 1] = __uint_as_float(w[c] & 0xffff0000u);
+                top = max(top, max(abs_bits(v[j + 2 * c]), abs_bits(v[j + 2 * c + 1])));
+            }
+        }
+        top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 16)));
+        top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 32)));
+        const int e = max(static_cast<int>(top >> 23), 11);
+        q.scale[i] = e == 255 ? 255 : e - 7;  // NaN or infinite: all is NaN
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) {
+            float r[4];
+            int hi = 0, lo = 0;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) r[c] = __builtin_amdgcn_ldexpf(v[j + c], 134 - e);
+            hi = __builtin_amdgcn_cvt_pk_fp8_f32(r[0], r[1], hi, false);
+            hi = __builtin_amdgcn_cvt_pk_fp8_f32(r[2], r[3], hi, true);
+            const auto h0 = __builtin_amdgcn_cvt_pk_f32_fp8(hi, false), h1 = __builtin_amdgcn_cvt_pk_f32_fp8(hi, true);
+            lo = __builtin_amdgcn_cvt_pk_fp8_f32((r[0] - h0[0]) * 16.0f, (r[1] - h0[1]) * 16.0f, lo, false);
+            lo = __builtin_amdgcn_cvt_pk_fp8_f32((r[2] - h1[0]) * 16.0f, (r[3] - h1[1]) * 16.0f, lo, true);
+            q.hi[i][j / 4] = hi;
+            q.lo[i][j / 4] = lo;
+        }
+    }
+}
+
+// c + codes x queries: rows are the 16 tokens, columns the 16 queries.
+template <int DP>
+__device__ __forceinline__ f32x4 scores(const Step<DP>& s, int a, const Queries<DP>& q) {
+    f32x4 c = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < Step<DP>::KB; ++i) {
+        const u32x4_t w = s.k[a][i];
+        const i32x8_t k = {static_cast<int>(w[0]), static_cast<int>(w[1]), static_cast<int>(w[2]), static_cast<int>(w[3]), 0, 0, 0, 0};
+        c = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(k, q.lo[i], c, 4, 0, 0, s.ks[a][i], 0, q.scale[i] == 255 ? 255 : q.scale[i] - 4);
+        c = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(k, q.hi[i], c, 4, 0, 0, s.ks[a][i], 0, q.scale[i]);
+    }
+    return c;
 }
 
 // A wave's state of RT * 16 queries: lane (n, g) holds, of query n, O at d = E (4 g + r) + i as o[][i][r].
@@ -220,37 +370,28 @@ struct State {
     float m[RT], l[RT];
 };
 
-template <int DP, int RT>
-__device__ __forceinline__ void attend(const Params& p, const Places<DP>& at, const Step<DP>& s, int seq, int head, int token,
-                                       int length, const int (&seen)[RT], int least, const u32x4_t (&q)[RT][DP / 32],
-                                       int lane, State<DP, RT>& st) {
-    constexpr int E = DP / 16, W = DP / 32;
+template <int DP, int RT, bool ONE>
+__device__ __forceinline__ void attend(const Params& p, const Places<DP>& at, const Step<DP>& s, const Where<ONE>& where, int seq,
+                                       int head, int token, int length, const int (&seen)[RT], int least,
+                                       const Queries<DP> (&q)[RT], int lane, State<DP, RT>& st) {
+    constexpr int E = DP / 16;
     const int g = lane >> 4;
     f32x4 score[RT][2];
 #pragma unroll
-    for (int a = 0; a < 2; ++a) {
+    for (int a = 0; a < 2; ++a)
 #pragma unroll
-        for (int r = 0; r < RT; ++r) score[r][a] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int c = 0; c < W; ++c) {
-            const float unit = __uint_as_float(s.ks[a][c / 4] << 23);
-            const uint32_t w = s.k[a][c];
-            const u32x4_t f = {two<0>(w, unit), two<1>(w, unit), two<2>(w, unit), two<3>(w, unit)};
-#pragma unroll
-            for (int r = 0; r < RT; ++r) score[r][a] = mma(f, q[r][c], score[r][a]);
-        }
-    }
+        for (int r = 0; r < RT; ++r) score[r][a] = scores<DP>(s, a, q[r]);
     uint32_t v[8][Step<DP>::VW];
     float unit[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         const uint32_t w = DP == 256 && at.second ? s.vs[j][Step<DP>::SW - 1] : s.vs[j][0];
-        unit[j] = __uint_as_float(__builtin_amdgcn_alignbit(w, w, at.turn[0]) & 0x7f800000u);
+        unit[j] = __uint_as_float(__builtin_amdgcn_alignbit(w, w, at.turn) & 0x7f800000u);
 #pragma unroll
         for (int w = 0; w < Step<DP>::VW; ++w) v[j][w] = s.v[j][w];
     }
     bool odd = false;  // a value that is NaN, of a token that not all queries may see
-    const bool masked = token + 32 > least || !s.there[0] || !s.there[1];
+    const bool masked = token + 32 > least || !where.has(0) || !where.has(1);
     if (masked) {
         asm volatile("");  // a branch around this stays one
 #pragma unroll
@@ -260,9 +401,9 @@ __device__ __forceinline__ void attend(const Params& p, const Places<DP>& at, co
                 const int t = token + 16 * a + 4 * g + j;
 #pragma unroll
                 for (int r = 0; r < RT; ++r)
-                    if (!s.there[a] || t >= seen[r]) score[r][a][j] = -__builtin_inff();
+                    if (!where.has(a) || t >= seen[r]) score[r][a][j] = -__builtin_inff();
                 // weights of 0 do not undo a NaN: it is taken out, and put back below where it is seen
-                const bool absent = !s.there[a] || t >= length, nan = unit[4 * a + j] == __builtin_inff();
+                const bool absent = !where.has(a) || t >= length, nan = unit[4 * a + j] == __builtin_inff();
                 odd |= !absent && nan;
                 if (absent || nan) {
                     unit[4 * a + j] = 1.0f;
@@ -353,11 +494,13 @@ __device__ __forceinline__ void attend(const Params& p, const Places<DP>& at, co
     }
 }
 
-// Fewer registers than the widest forms need would spill them.
-template <int DP, int RT>
-__global__ __launch_bounds__(256, DP * RT <= 128 ? 3 : DP * RT <= 256 ? 2 : 1) void kernel(Params p) {
-    constexpr int E = DP / 16, W = DP / 32;
-    __shared__ f32x4 area[2][RT * E][64];
+template <int DP, int RT, bool ONE>
+__global__ __launch_bounds__(256, resident(DP, RT)) void kernel(Params p) {
+    constexpr int E = DP / 16;
+    constexpr int STAGES = 4 * kStages * kStage<DP>, SUMS = 2 * RT * E * 64 * 16;  // of the waves' steps, then of their sums
+    __shared__ __attribute__((aligned(16))) uint8_t shared[STAGES > SUMS ? STAGES : SUMS];
+    const uint32_t lds = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t*)shared));
+    f32x4(*area)[RT * E][64] = reinterpret_cast<f32x4(*)[RT * E][64]>(shared);
     __shared__ float area_m[4][RT * 16], area_l[4][RT * 16];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 15, g = lane >> 4;
@@ -367,18 +510,20 @@ __global__ __launch_bounds__(256, DP * RT <= 128 ? 3 : DP * RT <= 256 ? 2 : 1) v
     for (int s = 64; s < p.sequences; s += 64) total += __shfl(units_upto(p, s, lane, &mine), 63);
     const Shares shares = shares_of(p, __builtin_amdgcn_readfirstlane(total));
     if (static_cast<int>(blockIdx.x) >= shares.workgroups) return;
-    int u = shares.start(blockIdx.x);
-    const int end = shares.start(blockIdx.x + 1);
+    int u = shares.begin(blockIdx.x);
+    const int end = shares.begin(blockIdx.x + 1);
     int seq = 0, before = 0;
     {
         const int x = u / pairs;
         if (p.sequences > 64) upto = units_upto(p, 0, lane, &mine);
         for (int s = 0; s < p.sequences; s += 64) {
+            const int mine_too = s + lane < p.sequences ? mine + shares.start : 0, last = min(64, p.sequences - s) - 1;
+            upto += shares.start * (min(lane, last) + 1);
             const unsigned long long past = __ballot(before + upto > x);
             if (past) {
                 const int at = __ffsll(past) - 1;
                 seq = s + at;
-                before += __shfl(upto - mine, at);
+                before += __shfl(upto - mine_too, at);
                 break;
             }
             before += __shfl(upto, 63);
@@ -388,49 +533,63 @@ __global__ __launch_bounds__(256, DP * RT <= 128 ? 3 : DP * RT <= 256 ? 2 : 1) v
     seq = __builtin_amdgcn_readfirstlane(seq);
     int length = __builtin_amdgcn_readfirstlane(length_of(p, seq));
     const int in_seq = __builtin_amdgcn_readfirstlane(u - before * pairs);
-    int pair = min(__builtin_amdgcn_readfirstlane(in_seq / units_of(length)), pairs - 1);
-    int first = __builtin_amdgcn_readfirstlane(in_seq - pair * units_of(length));
-    const Places<DP> at = places<DP>(p, lane);
+    int pair = min(__builtin_amdgcn_readfirstlane(in_seq / (shares.start + units_of(length))), pairs - 1);
+    // below 0: what only counts as units
+    int first = __builtin_amdgcn_readfirstlane(in_seq - pair * (shares.start + units_of(length))) - shares.start;
+    const uint32_t own = lds + wave * (kStages * kStage<DP>);
+    Places<DP> at = places<DP>(p, lane, own);
+    uint32_t stage = own;
+    int other = kStage<DP>;  // on from this stage to the other
     int slot = 2 * blockIdx.x;
     while (u < end) {
         const int all = units_of(length);
-        const int count = __builtin_amdgcn_readfirstlane(min(all - first, end - u));
+        int count = __builtin_amdgcn_readfirstlane(min(all - first, end - u));
+        u += count;
+        if (first < 0) {
+            count = max(count + first, 0);
+            first = 0;
+        }
+        if (count == 0) break;  // the last units of this workgroup, and none of tokens
         const int head = pair / p.row_blocks, row0 = (pair - head * p.row_blocks) * p.row_block;
         const int stop = min((first + count) * kUnit, length);
+        // While a step is worked on, out of registers, the next two are on their way to LDS.
+        int token = first * kUnit + wave * 32;
+        const int32_t* pages_of = p.table + static_cast<long long>(seq) * p.table_pitch;
+        auto place = [&](int t) __attribute__((always_inline)) { return where_is<ONE>(p, pages_of, head, t, t < stop ? length : 0); };
+        Where<ONE> here = place(token), next = place(token + kUnit);
+        barrier();  // the sums of the pair before have been read
+        copy_step<DP, ONE>(p, here, lane, stage);
+        copy_step<DP, ONE>(p, next, lane, stage + other);
         State<DP, RT> st;
-        u32x4_t q[RT][W];
+        Queries<DP> q[RT];
         int seen[RT];
         const int least = length - p.tokens + 1;
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
             const int row = row0 + r * 16 + n;
-            const int token = divide(min(row, p.rows - 1), p.per_group), h = head * p.group + min(row, p.rows - 1) - token * p.group;
-            seen[r] = least + token;
-            const bf16_t* x = p.q + seq * p.q_seq_stride + token * p.q_stride + h * p.q_head_stride;
-#pragma unroll
-            for (int c = 0; c < W; ++c) {
-                const int d = 8 * W * g + 8 * c;
-                q[r][c] = d < p.dim ? *reinterpret_cast<const u32x4_t*>(x + d) : u32x4_t{0, 0, 0, 0};
-            }
+            const int of = divide(min(row, p.rows - 1), p.per_group), h = head * p.group + min(row, p.rows - 1) - of * p.group;
+            seen[r] = least + of;
+            load_queries<DP>(p, p.q + seq * p.q_seq_stride + of * p.q_stride + h * p.q_head_stride, g, q[r]);
             st.m[r] = kLow;
             st.l[r] = 0.0f;
 #pragma unroll
             for (int i = 0; i < E; ++i) st.o[r][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         }
-        {
-            // two steps' codes in turn: while one is used, the other is on its way
-            Step<DP> even, uneven;
-            int token = first * kUnit + wave * 32;
-            load_step<DP>(p, at, seq, head, token < stop ? length : 0, token, even);
-            load_step<DP>(p, at, seq, head, token + kUnit < stop ? length : 0, token + kUnit, uneven);
-            for (; token < stop; token += 2 * kUnit) {
-                attend<DP, RT>(p, at, even, seq, head, token, length, seen, least, q, lane, st);
-                load_step<DP>(p, at, seq, head, token + 2 * kUnit < stop ? length : 0, token + 2 * kUnit, even);
-                if (token + kUnit >= stop) break;
-                attend<DP, RT>(p, at, uneven, seq, head, token + kUnit, length, seen, least, q, lane, st);
-                load_step<DP>(p, at, seq, head, token + 3 * kUnit < stop ? length : 0, token + 3 * kUnit, uneven);
-            }
+        for (; token < stop; token += kUnit) {
+            const Where<ONE> later = place(token + 2 * kUnit);
+            Step<DP> s;
+            wait_loads<kCopies<DP, ONE>>();
+            read_step<DP>(at, s);
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the step has been read: its stage may be filled again
+            copy_step<DP, ONE>(p, later, lane, stage);
+            attend<DP, RT, ONE>(p, at, s, here, seq, head, token, length, seen, least, q, lane, st);
+            here = next;
+            next = later;
+            stage += other;
+            move(at, other);
+            other = -other;
         }
+        wait_loads<0>();  // none is left on its way to LDS, which the sums take over
         // join the four waves: m first, then the sums, 2 and 3 into 0 and 1, 1 into 0
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
@@ -441,7 +600,7 @@ __global__ __launch_bounds__(256, DP * RT <= 128 ? 3 : DP * RT <= 256 ? 2 : 1) v
                 area_l[wave][r * 16 + n] = st.l[r];
             }
         }
-        __syncthreads();
+        barrier();
         float l[RT], m[RT];
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
@@ -459,7 +618,7 @@ __global__ __launch_bounds__(256, DP * RT <= 128 ? 3 : DP * RT <= 256 ? 2 : 1) v
                 if (wave >= 2) area[wave - 2][r * E + i][lane] = st.o[r][i];
             }
         }
-        __syncthreads();
+        barrier();
         if (wave < 2) {
 #pragma unroll
             for (int r = 0; r < RT; ++r)
@@ -469,7 +628,7 @@ __global__ __launch_bounds__(256, DP * RT <= 128 ? 3 : DP * RT <= 256 ? 2 : 1) v
                     if (wave == 1) area[1][r * E + i][lane] = st.o[r][i];
                 }
         }
-        __syncthreads();
+        barrier();
         if (wave == 0) {
 #pragma unroll
             for (int r = 0; r < RT; ++r) {
@@ -505,10 +664,8 @@ __global__ __launch_bounds__(256, DP * RT <= 128 ? 3 : DP * RT <= 256 ? 2 : 1) v
                 }
             }
         }
-        __syncthreads();
         slot = 2 * blockIdx.x + 1;
-        u += count;
-        first = 0;
+        first = -shares.start;
         if (++pair == pairs && u < end) {
             pair = 0;
             seq = min(seq + 1, p.sequences - 1);
@@ -520,8 +677,8 @@ __global__ __launch_bounds__(256, DP * RT <= 128 ? 3 : DP * RT <= 256 ? 2 : 1) v
 // Joins the parts of one query: grid (sequence and pair, row of its block), 256 threads.
 __global__ __launch_bounds__(256) void join_kernel(Params p) {
     __shared__ f32x4 area[256];
-    __shared__ float area_m[4], area_l[256];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    __shared__ float area_m[256], area_l[256];
+    const int lane = threadIdx.x & 63;
     const int pairs = p.kv_heads * p.row_blocks, seq = blockIdx.x / pairs, pair = blockIdx.x - seq * pairs;
     const int head = pair / p.row_blocks, in_block = blockIdx.y, row = (pair - head * p.row_blocks) * p.row_block + in_block;
     if (row >= p.rows) return;
@@ -539,40 +696,40 @@ __global__ __launch_bounds__(256) void join_kernel(Params p) {
         before += __shfl_xor(before, d);
     }
     const Shares shares = shares_of(p, n);
-    const int u0 = before * pairs + pair * mine, w0 = shares.owner(u0), w1 = shares.owner(u0 + mine - 1);
+    const int u0 = (before + shares.start * seq) * pairs + pair * (shares.start + mine) + shares.start;
+    const int w0 = shares.owner(u0), w1 = shares.owner(u0 + mine - 1);
     if (w0 == w1) return;
     auto place = [&](int w) {
-        const int slot = 2 * w + (shares.start(w) >= u0 ? 0 : 1);
+        const int slot = 2 * w + (shares.begin(w) >= u0 - shares.start ? 0 : 1);  // its first part, or its last
         return static_cast<long long>(slot) * p.row_block + in_block;
     };
-    float m = kLow;
-    for (int w = w0 + threadIdx.x; w <= w1; w += 256) m = fmaxf(m, p.part_ml[2 * place(w)]);
-#pragma unroll
-    for (int d = 32; d; d /= 2) m = fmaxf(m, __shfl_xor(m, d));
-    if (lane == 0) area_m[wave] = m;
-    __syncthreads();
-    m = fmaxf(fmaxf(area_m[0], area_m[1]), fmaxf(area_m[2], area_m[3]));
     const int across = p.dim / 4, strands = 256 / across;  // threads of a row, rows at a time
     const int strand = threadIdx.x / across, d = (threadIdx.x - strand * across) * 4;
     f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
-    float l = 0.0f;
+    float l = 0.0f, m = kLow;
     if (strand < strands) {
 #pragma unroll 4
         for (int w = w0 + strand; w <= w1; w += strands) {
             const long long at = place(w);
             const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * at);
-            const float f = __builtin_amdgcn_exp2f(ml.x - m);
-            l += ml.y * f;
-            sum += *reinterpret_cast<const f32x4*>(p.part + at * p.dim + d) * f;
+            const f32x4 o = *reinterpret_cast<const f32x4*>(p.part + at * p.dim + d);
+            const float to = fmaxf(m, ml.x), f = __builtin_amdgcn_exp2f(m - to), e = __builtin_amdgcn_exp2f(ml.x - to);
+            m = to;
+            l = l * f + ml.y * e;
+            sum = sum * f + o * e;
         }
     }
     area[threadIdx.x] = sum;
     area_l[threadIdx.x] = l;
+    area_m[threadIdx.x] = m;
     __syncthreads();
     if (strand != 0) return;
     for (int s = 1; s < strands; ++s) {
-        sum += area[s * across + threadIdx.x];
-        l += area_l[s * across + threadIdx.x];
+        const float ms = area_m[s * across + threadIdx.x], to = fmaxf(m, ms);
+        const float f = __builtin_amdgcn_exp2f(m - to), e = __builtin_amdgcn_exp2f(ms - to);
+        m = to;
+        l = l * f + area_l[s * across + threadIdx.x] * e;
+        sum = sum * f + area[s * across + threadIdx.x] * e;
     }
     const float inverse = l == 0.0f ? 0.0f : 1.0f / l;
     const int token = divide(row, p.per_group), h = head * p.group + row - token * p.group;
@@ -597,8 +754,7 @@ Plan plan(const cfwd_mx_cache_attention_desc* d, const cfwd_mx_cache* c) {
     const long long longest = static_cast<long long>(d->table_pitch) * c->page_size;
     const long long most = std::max(1ll, (longest + kUnit - 1) / kUnit);
     const long long units = most * d->sequences * c->kv_heads * r.row_blocks;
-    const int resident = r.dp * r.rt <= 128 ? 3 : r.dp * r.rt <= 256 ? 2 : 1;
-    r.workgroups = static_cast<int>(std::min<long long>(units, static_cast<long long>(compute_units()) * resident));
+    r.workgroups = static_cast<int>(std::min<long long>(units, static_cast<long long>(compute_units()) * decode::resident(r.dp, r.rt)));
     r.join = most > 1;
     if (r.join) {
         const size_t slots = 2 * static_cast<size_t>(r.workgroups) * r.rt * 16;
@@ -639,6 +795,8 @@ cfwd_status mx_cache_attention(const cfwd_mx_cache_attention_desc* d, const cfwd
     p.table_pitch = d->table_pitch;
     p.blocks = static_cast<int>(mx_blocks(c->head_dim));
     p.scale_pitch = static_cast<int>(mx_scale_pitch(c->head_dim));
+    p.page_codes = static_cast<uint32_t>(c->kv_heads) * c->page_size * p.blocks * 16;  // below 2^31, as checked
+    p.page_scales = static_cast<uint32_t>(c->kv_heads) * c->page_size * p.scale_pitch;
     p.rows = d->tokens * p.group;
     p.row_blocks = plan.row_blocks;
     p.row_block = plan.rt * 16;
@@ -649,18 +807,22 @@ cfwd_status mx_cache_attention(const cfwd_mx_cache_attention_desc* d, const cfwd
     p.q_head_stride = d->q_head_stride;
     p.page = mx::divisor(c->page_size);
     p.per_group = mx::divisor(p.group);
-    auto go = [&](auto kernel) { kernel<<<plan.workgroups, 256, 0, st>>>(p); };
+    const bool one = c->page_size % 32 == 0;
+    auto go = [&](auto whole, auto halves) {
+        if (one) whole<<<plan.workgroups, 256, 0, st>>>(p);
+        else halves<<<plan.workgroups, 256, 0, st>>>(p);
+    };
     if (plan.dp == 64) {
-        if (plan.rt == 1) go(decode::kernel<64, 1>);
-        else if (plan.rt == 2) go(decode::kernel<64, 2>);
-        else go(decode::kernel<64, 4>);
+        if (plan.rt == 1) go(decode::kernel<64, 1, true>, decode::kernel<64, 1, false>);
+        else if (plan.rt == 2) go(decode::kernel<64, 2, true>, decode::kernel<64, 2, false>);
+        else go(decode::kernel<64, 4, true>, decode::kernel<64, 4, false>);
     } else if (plan.dp == 128) {
-        if (plan.rt == 1) go(decode::kernel<128, 1>);
-        else if (plan.rt == 2) go(decode::kernel<128, 2>);
-        else go(decode::kernel<128, 4>);
+        if (plan.rt == 1) go(decode::kernel<128, 1, true>, decode::kernel<128, 1, false>);
+        else if (plan.rt == 2) go(decode::kernel<128, 2, true>, decode::kernel<128, 2, false>);
+        else go(decode::kernel<128, 4, true>, decode::kernel<128, 4, false>);
     } else {
-        if (plan.rt == 1) go(decode::kernel<256, 1>);
-        else go(decode::kernel<256, 2>);
+        if (plan.rt == 1) go(decode::kernel<256, 1, true>, decode::kernel<256, 1, false>);
+        else go(decode::kernel<256, 2, true>, decode::kernel<256, 2, false>);
     }
     cfwd_status e = check_hip(hipGetLastError(), "cache attention launch");
     if (e != CFWD_OK || !plan.join) return e;

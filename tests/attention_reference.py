@@ -8,6 +8,8 @@ Bounds.  fp32 has a rounding unit of u = 2^-24.
   rounding a product: dim u sum |q k|; times scale, and the weight's exponent is rounded to u of its size twice (the
   product with scale log2(e), whose own rounding it is, and the difference from the maximum).  A weight's relative error
   is then at most d = scale dim u sum |q k| + 3 u (|s| + |m|) + 2^-21 (the power of two), plus its rounding to bf16, 2^-8.
+  Over the cache a query enters in two 8-bit parts, exactly or within 2^-21 of its largest of 128 values, which adds
+  scale 2^-21 max |q| sum |k| to a score's error.
 * Output: o = sum w v / sum w with every w off by a relative r: off by sum w r (v - o) / sum w, and by a factor 1 + r
   (below 1.02) for what is of second order; the sums over n keys add n u of sum w |v| / sum w, joined parts 64 u; then
   one rounding to bf16, 2^-8 of the result.
@@ -50,8 +52,9 @@ def rotate(x, positions, axes, freq, adjacent):
     return y, size
 
 
-def attend(q, k, v, causal, scale):
-    """(output, bound before its own rounding) of one sequence: q [nq, heads, dim], k and v [nk, kv heads, dim]."""
+def attend(q, k, v, causal, scale, parts=False):
+    """(output, bound before its own rounding) of one sequence: q [nq, heads, dim], k and v [nk, kv heads, dim]; parts:
+    queries enter in two parts."""
     nq, heads, dim = q.shape
     nk, kv_heads, _ = k.shape
     out, bound = np.zeros(q.shape), np.zeros(q.shape)
@@ -67,6 +70,9 @@ def attend(q, k, v, causal, scale):
                 m = s.max()
                 w = np.exp(s - m)
                 r = scale * dim * U * (np.abs(keys) @ np.abs(q[i, h])) + 3 * U * (np.abs(s) + abs(m)) + 2.0 ** -21 + 2.0 ** -8
+                if parts:
+                    for d in range(0, dim, 128):
+                        r += scale * 2.0 ** -21 * np.abs(q[i, h, d:d + 128]).max() * np.abs(keys[:, d:d + 128]).sum(1)
                 w /= w.sum()
                 out[i, h] = w @ values
                 bound[i, h] = 1.02 * ((w * r) @ np.abs(values - out[i, h])) + (n + 64) * U * (w @ np.abs(values))

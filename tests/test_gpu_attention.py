@@ -238,7 +238,7 @@ def test_cache_attention(lengths, tokens, page, h, kh, dim):
     assert torch.equal(got, B.mx_cache_attention(q, paged.cache, paged.table, ints(torch, lengths)))
     for i in range(len(lengths)):
         k, v = paged.values(0, i), paged.values(1, i)
-        want, bound = A.attend(np64(q[i]), k, v, True, dim ** -0.5)
+        want, bound = A.attend(np64(q[i]), k, v, True, dim ** -0.5, parts=True)
         A.check(np64(got[i]), want, bound)
 
 
@@ -278,7 +278,7 @@ def test_cache_attention_bad_lengths_and_pages():
     got = B.mx_cache_attention(q, paged.cache, table, ints(torch, [64, 64]))
     assert not got[0].any()
     k, v = (np.concatenate([paged.values(w, 1)[:16], paged.values(w, 1)[48:]]) for w in (0, 1))
-    want, bound = A.attend(np64(q[1:]), k, v, False, 64 ** -0.5)
+    want, bound = A.attend(np64(q[1:]), k, v, False, 64 ** -0.5, parts=True)
     A.check(np64(got[1:]), want, bound)
 
 
