@@ -93,54 +93,54 @@ __device__ __forceinline__ int k_swizzle(int row) { return DP == 64 ? (row >> 1)
 template <int DP>
 __device__ __forceinline__ int v_swizzle(int row) { return DP == 64 ? ((row >> 1) & 1) * 4 : (row & 3) * 4; }
 
-// Rows of a sequence; the same for the whole wave.
+// Rows of a sequence.
 struct Range {
     int from, count;
 };
-__device__ __forceinline__ int count_of(const int32_t* starts, int seq, int tokens) {
-    const int a = min(max(starts[seq], 0), tokens);
-    return min(max(starts[seq + 1], a), tokens) - a;
-}
 __device__ __forceinline__ Range rows_of(const int32_t* starts, int seq, int tokens) {
-    const int a = min(max(starts[seq], 0), tokens), b = min(max(starts[seq + 1], a), tokens);
-    return {__builtin_amdgcn_readfirstlane(a), __builtin_amdgcn_readfirstlane(b - a)};
+    const int a = min(max(starts[seq], 0), tokens);
+    return {a, min(max(starts[seq + 1], a), tokens) - a};
 }
 
-// The sequence of the tile `tile`, counted from the last one back, and its tile; seq < 0: there is none.
+// A tile of rows, counted from the last sequence's last one back: its number in its sequence (below 0: there is none), and the
+// sequence's queries and keys.  The same for the whole wave; each lane looks at one sequence of 64.
 struct Place {
-    int seq, tile;
+    int tile;
+    Range q, k;
 };
 template <int BM>
-__device__ Place find_tile(const Params& p, int tile, int lane) {
-    int total = 0;
-    for (int s = 0; s < p.sequences; s += 64) {
-        int n = 0;
-        if (s + lane < p.sequences) n = (count_of(p.q_starts, s + lane, p.q_tokens) * p.group + BM - 1) / BM;
-        total += n;
+__device__ __forceinline__ Place find_tile(const Params& p, int tile, int lane) {
+    auto look = [&](int s, Range* q, Range* k) {
+        const int seq = min(s + lane, p.sequences - 1);
+        *q = rows_of(p.q_starts, seq, p.q_tokens);
+        *k = rows_of(p.k_starts, seq, p.k_tokens);
+        return s + lane < p.sequences ? (q->count * p.group + BM - 1) / BM : 0;
+    };
+    Range q, k;
+    int n = look(0, &q, &k), upto = wave_scan(n), total = __builtin_amdgcn_readlane(upto, 63);
+    for (int s = 64; s < p.sequences; s += 64) {
+        Range other;
+        total += __builtin_amdgcn_readlane(wave_scan(look(s, &other, &other)), 63);
     }
-#pragma unroll
-    for (int d = 32; d; d /= 2) total += __shfl_xor(total, d);
     const int x = total - 1 - tile;
-    if (x < 0) return {-1, 0};
+    Place r = {-1, {0, 0}, {0, 0}};
     int before = 0;
-    for (int s = 0; s < p.sequences; s += 64) {
-        int n = 0;
-        if (s + lane < p.sequences) n = (count_of(p.q_starts, s + lane, p.q_tokens) * p.group + BM - 1) / BM;
-        int upto = n;
-#pragma unroll
-        for (int d = 1; d < 64; d *= 2) {
-            const int o = __shfl_up(upto, d);
-            if (lane >= d) upto += o;
+    for (int s = 0; s < p.sequences && x >= 0; s += 64) {
+        if (s > 0) {
+            n = look(s, &q, &k);
+            upto = wave_scan(n);
         }
-        upto += before;
-        const unsigned long long past = __ballot(upto > x);
+        const unsigned long long past = __ballot(before + upto > x);
         if (past) {
             const int at = __ffsll(past) - 1;
-            return {s + at, x - __shfl(upto - n, at)};
+            r.tile = x - before - __builtin_amdgcn_readlane(upto - n, at);
+            r.q = {__builtin_amdgcn_readlane(q.from, at), __builtin_amdgcn_readlane(q.count, at)};
+            r.k = {__builtin_amdgcn_readlane(k.from, at), __builtin_amdgcn_readlane(k.count, at)};
+            break;
         }
-        before = __shfl(upto, 63);
+        before += __builtin_amdgcn_readlane(upto, 63);
     }
-    return {-1, 0};
+    return r;
 }
 
 template <int N>
@@ -157,10 +157,9 @@ __global__ __launch_bounds__(64 * WAVES, SIMD_WAVES) void kernel(Params p) {
     const int n = lane & 31, h = lane >> 5;
     const int head = blockIdx.x % p.kv_heads;
     const Place place = find_tile<BM>(p, blockIdx.x / p.kv_heads, lane);
-    const int seq = __builtin_amdgcn_readfirstlane(place.seq);
-    if (seq < 0) return;
-    const int row0 = __builtin_amdgcn_readfirstlane(place.tile) * BM;
-    const Range qs = rows_of(p.q_starts, seq, p.q_tokens), ks = rows_of(p.k_starts, seq, p.k_tokens);
+    if (place.tile < 0) return;
+    const int row0 = place.tile * BM;
+    const Range qs = place.q, ks = place.k;
     const int rows = qs.count * p.group;
     // row r sees the keys before offset + r / group + 1, and before ks.count
     const int offset = ks.count - qs.count;

@@ -71,16 +71,10 @@ __device__ __forceinline__ int length_of(const Params& p, int seq) {
 }
 __device__ __forceinline__ int units_of(int length) { return max(1, (length + kUnit - 1) / kUnit); }
 
-// Units of one head, over all sequences: of those up to and with this lane's of the 64 from s on.
-__device__ __forceinline__ int units_upto(const Params& p, int s, int lane, int* mine) {
-    *mine = s + lane < p.sequences ? units_of(length_of(p, s + lane)) : 0;
-    int v = *mine;
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-        const int o = __shfl_up(v, d);
-        if (lane >= d) v += o;
-    }
-    return v;
+// Units of one head in the sequence of this lane, of the 64 from s on, and its length.
+__device__ __forceinline__ int units_at(const Params& p, int s, int lane, int* length) {
+    *length = length_of(p, min(s + lane, p.sequences - 1));
+    return s + lane < p.sequences ? units_of(*length) : 0;
 }
 
 // The units of all pairs (head, block of rows) of all sequences, shared out: workgroup w takes `most` or one less of them,
@@ -506,36 +500,38 @@ __global__ __launch_bounds__(256, resident(DP, RT)) void kernel(Params p) {
     const int n = lane & 15, g = lane >> 4;
     const int pairs = p.kv_heads * p.row_blocks;  // of a sequence: (head, block of rows)
     // the units of all sequences, then the sequence in which the first unit of this workgroup lies
-    int mine, upto = units_upto(p, 0, lane, &mine), total = __shfl(upto, 63);
-    for (int s = 64; s < p.sequences; s += 64) total += __shfl(units_upto(p, s, lane, &mine), 63);
-    const Shares shares = shares_of(p, __builtin_amdgcn_readfirstlane(total));
+    int its, mine = units_at(p, 0, lane, &its), upto = wave_scan(mine), total = __builtin_amdgcn_readlane(upto, 63);
+    for (int s = 64; s < p.sequences; s += 64) {
+        int unused;
+        total += __builtin_amdgcn_readlane(wave_scan(units_at(p, s, lane, &unused)), 63);
+    }
+    const Shares shares = shares_of(p, total);
     if (static_cast<int>(blockIdx.x) >= shares.workgroups) return;
     int u = shares.begin(blockIdx.x);
     const int end = shares.begin(blockIdx.x + 1);
-    int seq = 0, before = 0;
+    int seq = 0, before = 0, length = 0;
     {
         const int x = u / pairs;
-        if (p.sequences > 64) upto = units_upto(p, 0, lane, &mine);
         for (int s = 0; s < p.sequences; s += 64) {
-            const int mine_too = s + lane < p.sequences ? mine + shares.start : 0, last = min(64, p.sequences - s) - 1;
-            upto += shares.start * (min(lane, last) + 1);
-            const unsigned long long past = __ballot(before + upto > x);
+            if (s > 0) {
+                mine = units_at(p, s, lane, &its);
+                upto = wave_scan(mine);
+            }
+            const int last = min(64, p.sequences - s) - 1, with = upto + shares.start * (min(lane, last) + 1);
+            const unsigned long long past = __ballot(before + with > x);
             if (past) {
                 const int at = __ffsll(past) - 1;
                 seq = s + at;
-                before += __shfl(upto - mine_too, at);
+                length = __builtin_amdgcn_readlane(its, at);
+                before += __builtin_amdgcn_readlane(with - mine - shares.start, at);
                 break;
             }
-            before += __shfl(upto, 63);
-            upto = units_upto(p, s + 64, lane, &mine);
+            before += __builtin_amdgcn_readlane(with, 63);
         }
     }
-    seq = __builtin_amdgcn_readfirstlane(seq);
-    int length = __builtin_amdgcn_readfirstlane(length_of(p, seq));
-    const int in_seq = __builtin_amdgcn_readfirstlane(u - before * pairs);
-    int pair = min(__builtin_amdgcn_readfirstlane(in_seq / (shares.start + units_of(length))), pairs - 1);
-    // below 0: what only counts as units
-    int first = __builtin_amdgcn_readfirstlane(in_seq - pair * (shares.start + units_of(length))) - shares.start;
+    const int in_seq = u - before * pairs, each = shares.start + units_of(length);
+    int pair = min(in_seq / each, pairs - 1);
+    int first = in_seq - pair * each - shares.start;  // below 0: what only counts as units
     const uint32_t own = lds + wave * (kStages * kStage<DP>);
     Places<DP> at = places<DP>(p, lane, own);
     uint32_t stage = own;
