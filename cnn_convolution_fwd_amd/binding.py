@@ -1068,6 +1068,8 @@ def _int32(dev: int, t, shape, what: str):
     _check_on(dev, t)
 
 
+# Outputs are allocated with new_empty from a plain tuple, 0.9 us a tensor under torch.empty with dtype and device named.
+
 def _heads_of(t, what: str) -> Tuple[int, int, int, int, int]:
     """(tokens, heads, dim, token stride, head stride) of [tokens, heads, dim] with dense dims; the stride of an axis of
     one, which may be any number, as in a dense tensor."""
@@ -1101,20 +1103,22 @@ def rope(q, k, positions, table: RopeTable, adjacent: bool = False, q_out=None, 
     tokens, heads, dim, qs, qh = _heads_of(q, "q")
     code = _float_code(q)
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        q_out, qos, qoh = q.new_empty((tokens, heads, dim)), heads * dim, dim
     elif q_out.shape != q.shape or q_out.dtype != q.dtype or q_out.get_device() != dev:
         raise ValueError("q_out must be as q")
-    _, _, _, qos, qoh = _heads_of(q_out, "q_out")
+    else:
+        _, _, _, qos, qoh = _heads_of(q_out, "q_out")
     kh = ks = khs = kos = koh = 0
     if k is not None:
         kt, kh, kd, ks, khs = _heads_of(k, "k")
         if kt != tokens or kd != dim or k.dtype != q.dtype or k.get_device() != dev:
             raise ValueError("k must have q's tokens, dim, dtype and device")
         if k_out is None:
-            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+            k_out, kos, koh = k.new_empty((tokens, kh, dim)), kh * dim, dim
         elif k_out.shape != k.shape or k_out.dtype != k.dtype or k_out.get_device() != dev:
             raise ValueError("k_out must be as k")
-        _, _, _, kos, koh = _heads_of(k_out, "k_out")
+        else:
+            _, _, _, kos, koh = _heads_of(k_out, "k_out")
     elif k_out is not None:
         raise ValueError("k_out without k")
     pairs, axes = table
@@ -1151,21 +1155,24 @@ def mx_cache(pages: int, page_size: int, heads: int, dim: int, device="cuda") ->
 
 
 def _check_cache(cache: MxCache):
-    """(GPU, sizes (pages, page_size, heads, dim), addresses) of a cache whose parts fit each other."""
+    """(GPU, sizes (pages, page_size, heads, dim), descriptor of the cache) of one whose parts fit each other."""
     if not isinstance(cache, MxCache):
         raise TypeError("cache must be an MxCache")
     (kc, ks, dim), (vc, vs, v_dim) = cache
     shape, u8 = kc.shape, _torch().uint8
+    if len(shape) != 4:
+        raise ValueError("the cache's parts must be MxTensors [pages, heads, page_size, dim] of one shape")
+    pages, heads, page_size, pitch = shape
     cp, sp = mx_pitches(dim)
-    lead = shape[:-1]
-    if len(shape) != 4 or v_dim != dim or vc.shape != shape or shape[3] != cp or not cp or ks.shape != (*lead, sp) \
+    if v_dim != dim or vc.shape != shape or pitch != cp or not cp or ks.shape != (pages, heads, page_size, sp) \
             or vs.shape != ks.shape:
         raise ValueError("the cache's parts must be MxTensors [pages, heads, page_size, dim] of one shape")
     if kc.dtype != u8 or ks.dtype != u8 or vc.dtype != u8 or vs.dtype != u8:
         raise TypeError("codes and scales must be uint8")
     dev = kc.get_device()
     _check_on(dev, kc, ks, vc, vs)
-    return dev, (lead[0], lead[2], lead[1], dim), (kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr())
+    return dev, (pages, page_size, heads, dim), ctypes.byref(MxCacheParts(
+        pages, page_size, heads, dim, kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr()))
 
 
 @functools.lru_cache(maxsize=1024)
@@ -1195,9 +1202,8 @@ def mx_cache_write(k, v, cache: MxCache, slots):
     if guard is not None:
         with guard:
             return mx_cache_write(k, v, cache, slots)
-    _check(_lib().cfwd_mx_cache_write(_mx_cache_write_desc(tokens, code, wide, ks, kh, vs, vh),
-                                      ctypes.byref(MxCacheParts(*sizes, *parts)), k.data_ptr(), v.data_ptr(),
-                                      slots.data_ptr(), _stream_of(dev)))
+    _check(_lib().cfwd_mx_cache_write(_mx_cache_write_desc(tokens, code, wide, ks, kh, vs, vh), parts, k.data_ptr(),
+                                      v.data_ptr(), slots.data_ptr(), _stream_of(dev)))
 
 
 @functools.lru_cache(maxsize=1024)
@@ -1230,9 +1236,9 @@ def mx_cache_read(cache: MxCache, page_table, starts, tokens: int, dtype="bf16",
             code = _code(_MX_CODES, dtype, "dtype")
             if code == MXFP4:
                 raise ValueError("dtype must be f32 or bf16")
-            out = torch.empty(shape, dtype=torch.float32 if code == F32 else torch.bfloat16, device=cache.k.codes.device)
+            out = cache.k.codes.new_empty(shape, dtype=torch.float32 if code == F32 else torch.bfloat16)
         else:
-            if tuple(out.shape) != shape:
+            if out.shape != shape:
                 raise ValueError("outputs must have the shape %s" % (shape,))
             _check_on(dev, out)
         outs.append(out)
@@ -1243,20 +1249,19 @@ def mx_cache_read(cache: MxCache, page_table, starts, tokens: int, dtype="bf16",
     if guard is not None:
         with guard:
             return mx_cache_read(cache, page_table, starts, tokens, dtype, *outs)
-    _check(_lib().cfwd_mx_cache_read(_mx_cache_read_desc(shape[0], sequences, pitch, code),
-                                     ctypes.byref(MxCacheParts(*sizes, *parts)), page_table.data_ptr(),
+    _check(_lib().cfwd_mx_cache_read(_mx_cache_read_desc(shape[0], sequences, pitch, code), parts, page_table.data_ptr(),
                                      starts.data_ptr(), outs[0].data_ptr(), outs[1].data_ptr(), _stream_of(dev)))
     return outs[0], outs[1]
 
 
-def _workspace(workspace, need: int, device, dev: int):
-    """(tensor, address, bytes) of the caller's workspace, or of a new one where one is needed."""
+def _workspace(workspace, need: int, like, dev: int):
+    """(tensor, address, bytes) of the caller's workspace, or of a new one where one is needed, on ``like``'s GPU."""
     if workspace is not None:
         _check_on(dev, workspace)
         return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
     if not need:
         return None, None, 0
-    workspace = _torch().empty(need, dtype=_torch().uint8, device=device)
+    workspace = like.new_empty((-(-need // like.element_size()),))
     return workspace, workspace.data_ptr(), need
 
 
@@ -1278,7 +1283,6 @@ def mx_cache_attention(q, cache: MxCache, page_table, lengths, scale: Optional[f
     (the new tokens, which are in the cache already, among them).  ``scale``: default dim^-0.5.
     ``workspace`` (uint8, bytes as ``cfwd_mx_cache_attention_workspace_size`` says) is allocated when not given.
     """
-    torch = _torch()
     dev, sizes, parts = _check_cache(cache)
     if q.dim() not in (3, 4):
         raise ValueError("q must be [sequences, heads, dim] or [sequences, tokens, heads, dim]")
@@ -1300,7 +1304,7 @@ def mx_cache_attention(q, cache: MxCache, page_table, lengths, scale: Optional[f
     _int32(dev, lengths, (sequences,), "lengths")
     code = _float_code(q)
     if out is None:
-        out = torch.empty(shape, dtype=q.dtype, device=q.device)
+        out = q.new_empty(tuple(shape))
     else:
         if out.shape != shape or out.dtype != q.dtype:
             raise ValueError("out must be as q")
@@ -1312,10 +1316,9 @@ def mx_cache_attention(q, cache: MxCache, page_table, lengths, scale: Optional[f
             return mx_cache_attention(q, cache, page_table, lengths, scale, out, workspace)
     desc, need = _mx_cache_attention_desc(dev, sizes, sequences, tokens, heads, pitch, scale, code, seq_stride,
                                           token_stride, head_stride)
-    workspace, ws, ws_bytes = _workspace(workspace, need, q.device, dev)
-    _check(_lib().cfwd_mx_cache_attention(desc, ctypes.byref(MxCacheParts(*sizes, *parts)), q.data_ptr(),
-                                          page_table.data_ptr(), lengths.data_ptr(), out.data_ptr(), ws, ws_bytes,
-                                          _stream_of(dev)))
+    workspace, ws, ws_bytes = _workspace(workspace, need, q, dev)
+    _check(_lib().cfwd_mx_cache_attention(desc, parts, q.data_ptr(), page_table.data_ptr(), lengths.data_ptr(),
+                                          out.data_ptr(), ws, ws_bytes, _stream_of(dev)))
     return out
 
 
@@ -1338,7 +1341,6 @@ def attention(q, k, v, q_starts, k_starts=None, causal: bool = True, scale: Opti
     default dim^-0.5.  Rows of ``out`` behind the last sequence are left as they were (undefined where the call
     allocates it).  ``workspace`` (uint8, bytes as ``cfwd_attention_workspace_size`` says) is allocated when not given.
     """
-    torch = _torch()
     dev = q.get_device()
     tokens, heads, dim, qs, qh = _heads_of(q, "q")
     kt, kv_heads, kd, ks, kh = _heads_of(k, "k")
@@ -1356,7 +1358,7 @@ def attention(q, k, v, q_starts, k_starts=None, causal: bool = True, scale: Opti
     _int32(dev, k_starts, (sequences + 1,), "k_starts")
     code = _float_code(q)
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        out = q.new_empty((tokens, heads, dim))
     else:
         if out.shape != q.shape or out.dtype != q.dtype:
             raise ValueError("out must be as q")
@@ -1368,7 +1370,7 @@ def attention(q, k, v, q_starts, k_starts=None, causal: bool = True, scale: Opti
             return attention(q, k, v, q_starts, k_starts, causal, scale, out, workspace)
     desc, need = _attention_desc(dev, tokens, kt, sequences, heads, kv_heads, dim, int(bool(causal)), scale, code, qs, qh,
                                  ks, kh, vs, vh)
-    workspace, ws, ws_bytes = _workspace(workspace, need, q.device, dev)
+    workspace, ws, ws_bytes = _workspace(workspace, need, q, dev)
     _check(_lib().cfwd_attention(desc, q.data_ptr(), k.data_ptr(), v.data_ptr(), q_starts.data_ptr(),
                                  k_starts.data_ptr(), out.data_ptr(), ws, ws_bytes, _stream_of(dev)))
     return out
