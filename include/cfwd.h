@@ -554,8 +554,12 @@ cfwd_status cfwd_mx_cache_read(const cfwd_mx_cache_read_desc *desc, const cfwd_m
  * seen; a query that sees nothing gives 0.  head_dim: a multiple of 32 up to
  * 256; page_size: a multiple of 16; tokens <= 1024; q_heads a multiple of kv_heads; q 16-byte aligned with strides
  * that are multiples of 8 elements.
- * Products are exact and summed in fp32, as are the softmax's sums; its weights are rounded to bf16 before the product
- * with V. */
+ * Queries meet the cache's codes in two parts of 8 bits: exactly, but for values under 2^-13 of the largest of their 128,
+ * which are within 2^-21 of it.  Products are exact and summed in fp32, as are the softmax's sums; its weights are rounded
+ * to bf16 before the product with V.  A NaN in a key that a query sees makes that query's output NaN, one in a value its
+ * column; the others keep their bits.
+ * CFWD_ERR_UNSUPPORTED for other types and sizes, pages of 2^31 bytes of codes or more, and page tables that stand for 2^31
+ * or more pairs of 128 tokens and 16 queries. */
 typedef struct {
     int sequences, tokens, q_heads, table_pitch;
     float scale; /* > 0 */
@@ -578,7 +582,8 @@ cfwd_status cfwd_mx_cache_attention(const cfwd_mx_cache_attention_desc *desc, co
  * causal: the last query sees every key, the one before it one fewer, and so
  * on; a query that sees no key gives 0.  Rows of o behind the last sequence are
  * not written.  bf16; head_dim a multiple of 8 up to 256; q_heads a multiple of kv_heads; tensors 16-byte aligned, strides
- * multiples of 8 elements, k and v strides at most 2^24.  Roundings as in cfwd_mx_cache_attention. */
+ * multiples of 8 elements, k and v strides from head_dim to 2^24 (CFWD_ERR_UNSUPPORTED for others).  Products are exact and
+ * summed in fp32, as are the softmax's sums; its weights are rounded to bf16 before the product with v. */
 typedef struct {
     long long q_tokens, k_tokens;
     int sequences, q_heads, kv_heads, head_dim;
