@@ -495,8 +495,12 @@ Plan plan(const cfwd_attention_desc* d) {
     // sequences of x rows in all have at most (x + n (bm - 1)) / bm tiles, n of them not empty
     auto tiles = [&](int bm) { return (d->q_tokens * group + std::min<long long>(d->sequences, d->q_tokens) * (bm - 1)) / bm; };
     r.tiles = tiles(128);
-    const long long keys = d->k_tokens / std::max(1, d->sequences);
-    r.splits = static_cast<int>(std::max(1ll, std::min({2 * cus / (r.tiles * d->kv_heads), keys / 256, 64ll})));
+    // Two workgroups a CU from parts of 512 keys on, else one from parts of 256 on (32 heads over 8, us: 16 queries over 2000 keys
+    // 20 by 512 and 15 by 256, over 16400 32 with 64 parts and 27 with 32; 512 over 8700 91 with one a CU and 85 with two; 1000 over
+    // themselves 38 in two parts and 25 in one).
+    const long long whole = r.tiles * d->kv_heads, n = std::max(1, d->sequences);
+    const long long keys = std::max(0ll, d->k_tokens - (d->causal ? d->q_tokens / 2 : 0)) / n;  // that a query sees, on average
+    r.splits = static_cast<int>(std::max({1ll, std::min(cus / whole, keys / 256), std::min(2 * cus / whole, keys / 512)}));
     if (r.splits > 1) {
         const size_t n = static_cast<size_t>(d->q_tokens) * d->q_heads * r.splits;
         r.part_bytes = (n * d->head_dim * 4 + 255) / 256 * 256;

@@ -25,10 +25,11 @@
 // workgroups fit a CU instead of four.
 //
 // Work is split by the lengths, which only the device knows: a unit is 128
-// tokens of one sequence and head, every workgroup counts all units and takes an
+// tokens of one sequence and head, or several times that, every workgroup counts all units and takes an
 // equal run of them, which may end within one head and begin within another.  What
 // covers a head only in part leaves its sum, m and l in the workspace, and a
-// second launch joins these in the order of the tokens.
+// second launch joins these in the order of the tokens.  Where the page table has room for few tokens only,
+// a workgroup takes a head as a whole, and one launch is all.
 #include "attention.h"
 #include "mx.h"
 
@@ -40,12 +41,14 @@ namespace decode {
 
 using namespace mx;
 
-constexpr int kUnit = 128;      // tokens: a step of 32 for each of a workgroup's four waves
+constexpr int kRound = 128;  // tokens: a step of 32 for each of a workgroup's four waves
 constexpr int kStart = 3;
+constexpr int kLargest = 32;  // rounds of a unit
 constexpr float kLow = -3.0e38f;  // m before any score: finite, so that differences are numbers
 constexpr float kMost = 4096.0f;  // a lane's 8 weights sum up to this before m follows the scores
 
-// Workgroups on a CU: what registers (and LDS) allow without spilling, for heads of dp values and rt * 16 queries at once.
+// Workgroups on a CU: what registers (and LDS) allow without spilling (but five of 64 x 64), for heads of dp values and rt * 16
+// queries at once.
 constexpr int resident(int dp, int rt) { return dp * rt > 256 ? 1 : dp * rt > 128 ? 2 : rt == 1 ? 4 : 3; }
 
 struct Params {
@@ -59,7 +62,7 @@ struct Params {
     int blocks, scale_pitch;  // of a row: code blocks, bytes of scales
     uint32_t page_codes, page_scales;  // bytes of a page
     int rows, row_blocks, row_block;  // queries of a cache's head, in blocks of row_block
-    int workgroups;
+    int workgroups, whole, few;
     float scale2;  // scale * log2(e)
     long long q_seq_stride, q_stride, q_head_stride;
     Divisor page, per_group;
@@ -69,12 +72,21 @@ __device__ __forceinline__ int length_of(const Params& p, int seq) {
     const long long most = static_cast<long long>(p.table_pitch) * p.page_size;
     return static_cast<int>(min(static_cast<long long>(max(p.lengths[seq], 0)), most));
 }
-__device__ __forceinline__ int units_of(int length) { return max(1, (length + kUnit - 1) / kUnit); }
+__device__ __forceinline__ int rounds_of(int length) { return max(1, (length + kRound - 1) / kRound); }
 
-// Units of one head in the sequence of this lane, of the 64 from s on, and its length.
-__device__ __forceinline__ int units_at(const Params& p, int s, int lane, int* length) {
+// Rounds of one head in the sequence of this lane, of the 64 from s on, and its length.
+__device__ __forceinline__ int rounds_at(const Params& p, int s, int lane, int* length) {
     *length = length_of(p, min(s + lane, p.sequences - 1));
-    return s + lane < p.sequences ? units_of(*length) : 0;
+    return s + lane < p.sequences ? rounds_of(*length) : 0;
+}
+
+// Rounds of a unit, from those of one head in all sequences.  Where units of many rounds still give a part of the device's
+// workgroups one each, there are fewer parts to begin and to join; where there is more to do, equal runs of the
+// smallest units balance the workgroups (heads of 128, 8 of the cache; us: 1 sequence of 16000 tokens 18 by single rounds, 14 by 4,
+// 8 of up to 8000 tokens 24 and 20 by 8; 64 of up to 8192 69 and 72 by 32).
+__device__ __forceinline__ int unit_of(const Params& p, int rounds) {
+    const long long all = static_cast<long long>(rounds) * (p.kv_heads * p.row_blocks);
+    return all <= static_cast<long long>(p.few) * kLargest ? static_cast<int>((all + p.few - 1) / p.few) : 1;
 }
 
 // The units of all pairs (head, block of rows) of all sequences, shared out: workgroup w takes `most` or one less of them,
@@ -499,22 +511,39 @@ __global__ __launch_bounds__(256, resident(DP, RT)) void kernel(Params p) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 15, g = lane >> 4;
     const int pairs = p.kv_heads * p.row_blocks;  // of a sequence: (head, block of rows)
-    // the units of all sequences, then the sequence in which the first unit of this workgroup lies
-    int its, mine = units_at(p, 0, lane, &its), upto = wave_scan(mine), total = __builtin_amdgcn_readlane(upto, 63);
-    for (int s = 64; s < p.sequences; s += 64) {
-        int unused;
-        total += __builtin_amdgcn_readlane(wave_scan(units_at(p, s, lane, &unused)), 63);
-    }
-    const Shares shares = shares_of(p, total);
-    if (static_cast<int>(blockIdx.x) >= shares.workgroups) return;
-    int u = shares.begin(blockIdx.x);
-    const int end = shares.begin(blockIdx.x + 1);
-    int seq = 0, before = 0, length = 0;
-    {
+    int u = blockIdx.x, end = u + 1;
+    int seq = 0, length, unit = 0, pair, first;
+    Shares shares{};
+    if (p.whole) {  // a pair for each workgroup
+        seq = u / pairs;
+        pair = u - seq * pairs;
+        first = 0;
+        length = __builtin_amdgcn_readfirstlane(length_of(p, seq));
+        unit = rounds_of(length);
+    } else {
+        // the units of all sequences, then the sequence in which the first unit of this workgroup lies
+        int its, rounds = rounds_at(p, 0, lane, &its), total = __builtin_amdgcn_readlane(wave_scan(rounds), 63);
+        for (int s = 64; s < p.sequences; s += 64) {
+            int unused;
+            total += __builtin_amdgcn_readlane(wave_scan(rounds_at(p, s, lane, &unused)), 63);
+        }
+        unit = unit_of(p, total);
+        int mine = (rounds + unit - 1) / unit, upto = wave_scan(mine);
+        total = __builtin_amdgcn_readlane(upto, 63);
+        for (int s = 64; s < p.sequences; s += 64) {
+            int unused;
+            total += __builtin_amdgcn_readlane(wave_scan((rounds_at(p, s, lane, &unused) + unit - 1) / unit), 63);
+        }
+        shares = shares_of(p, total);
+        if (u >= shares.workgroups) return;
+        end = shares.begin(u + 1);
+        u = shares.begin(u);
+        int before = 0;
+        length = 0;
         const int x = u / pairs;
         for (int s = 0; s < p.sequences; s += 64) {
             if (s > 0) {
-                mine = units_at(p, s, lane, &its);
+                mine = (rounds_at(p, s, lane, &its) + unit - 1) / unit;
                 upto = wave_scan(mine);
             }
             const int last = min(64, p.sequences - s) - 1, with = upto + shares.start * (min(lane, last) + 1);
@@ -528,17 +557,17 @@ __global__ __launch_bounds__(256, resident(DP, RT)) void kernel(Params p) {
             }
             before += __builtin_amdgcn_readlane(with, 63);
         }
+        const int in_seq = u - before * pairs, each = shares.start + (rounds_of(length) + unit - 1) / unit;
+        pair = min(in_seq / each, pairs - 1);
+        first = in_seq - pair * each - shares.start;  // below 0: what only counts as units
     }
-    const int in_seq = u - before * pairs, each = shares.start + units_of(length);
-    int pair = min(in_seq / each, pairs - 1);
-    int first = in_seq - pair * each - shares.start;  // below 0: what only counts as units
     const uint32_t own = lds + wave * (kStages * kStage<DP>);
     Places<DP> at = places<DP>(p, lane, own);
     uint32_t stage = own;
     int other = kStage<DP>;  // on from this stage to the other
     int slot = 2 * blockIdx.x;
     while (u < end) {
-        const int all = units_of(length);
+        const int all = (rounds_of(length) + unit - 1) / unit;
         int count = __builtin_amdgcn_readfirstlane(min(all - first, end - u));
         u += count;
         if (first < 0) {
@@ -547,12 +576,12 @@ __global__ __launch_bounds__(256, resident(DP, RT)) void kernel(Params p) {
         }
         if (count == 0) break;  // the last units of this workgroup, and none of tokens
         const int head = pair / p.row_blocks, row0 = (pair - head * p.row_blocks) * p.row_block;
-        const int stop = min((first + count) * kUnit, length);
+        const int stop = min((first + count) * unit * kRound, length);
         // While a step is worked on, out of registers, the next two are on their way to LDS.
-        int token = first * kUnit + wave * 32;
+        int token = first * unit * kRound + wave * 32;
         const int32_t* pages_of = p.table + static_cast<long long>(seq) * p.table_pitch;
         auto place = [&](int t) __attribute__((always_inline)) { return where_is<ONE>(p, pages_of, head, t, t < stop ? length : 0); };
-        Where<ONE> here = place(token), next = place(token + kUnit);
+        Where<ONE> here = place(token), next = place(token + kRound);
         barrier();  // the sums of the pair before have been read
         copy_step<DP, ONE>(p, here, lane, stage);
         copy_step<DP, ONE>(p, next, lane, stage + other);
@@ -571,8 +600,8 @@ __global__ __launch_bounds__(256, resident(DP, RT)) void kernel(Params p) {
 #pragma unroll
             for (int i = 0; i < E; ++i) st.o[r][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         }
-        for (; token < stop; token += kUnit) {
-            const Where<ONE> later = place(token + 2 * kUnit);
+        for (; token < stop; token += kRound) {
+            const Where<ONE> later = place(token + 2 * kRound);
             Step<DP> s;
             wait_loads<kCopies<DP, ONE>>();
             read_step<DP>(at, s);
@@ -678,19 +707,22 @@ __global__ __launch_bounds__(256) void join_kernel(Params p) {
     const int pairs = p.kv_heads * p.row_blocks, seq = blockIdx.x / pairs, pair = blockIdx.x - seq * pairs;
     const int head = pair / p.row_blocks, in_block = blockIdx.y, row = (pair - head * p.row_blocks) * p.row_block + in_block;
     if (row >= p.rows) return;
-    const int mine = units_of(length_of(p, seq));
-    if (mine == 1) return;
-    int n = 0, before = 0;
-    for (int s = lane; s < p.sequences; s += 64) {
-        const int c = units_of(length_of(p, s));
-        n += c;
-        before += s < seq ? c : 0;
-    }
-#pragma unroll
-    for (int d = 32; d; d /= 2) {
-        n += __shfl_xor(n, d);
-        before += __shfl_xor(before, d);
-    }
+    const int rounds = rounds_of(length_of(p, seq));
+    if (rounds == 1) return;
+    auto count = [&](int unit, int* before) {  // units of a head in all sequences, and in those before this
+        int n = 0, b = 0;
+        for (int s = lane; s < p.sequences; s += 64) {
+            const int c = (rounds_of(length_of(p, s)) + unit - 1) / unit;
+            n += c;
+            b += s < seq ? c : 0;
+        }
+        *before = __builtin_amdgcn_readlane(wave_scan(b), 63);
+        return __builtin_amdgcn_readlane(wave_scan(n), 63);
+    };
+    int before;
+    int n = count(1, &before);
+    const int unit = unit_of(p, n), mine = (rounds + unit - 1) / unit;
+    if (unit > 1) n = count(unit, &before);
     const Shares shares = shares_of(p, n);
     const int u0 = (before + shares.start * seq) * pairs + pair * (shares.start + mine) + shares.start;
     const int w0 = shares.owner(u0), w1 = shares.owner(u0 + mine - 1);
@@ -736,7 +768,7 @@ __global__ __launch_bounds__(256) void join_kernel(Params p) {
 }
 
 struct Plan {
-    int dp, rt, row_blocks, workgroups;
+    int dp, rt, row_blocks, workgroups, few;
     bool join;
     size_t part_bytes, bytes;
 };
@@ -748,10 +780,15 @@ Plan plan(const cfwd_mx_cache_attention_desc* d, const cfwd_mx_cache* c) {
     r.rt = rows <= 16 ? 1 : rows <= 32 || r.dp == 256 ? 2 : 4;
     r.row_blocks = (rows + r.rt * 16 - 1) / (r.rt * 16);
     const long long longest = static_cast<long long>(d->table_pitch) * c->page_size;
-    const long long most = std::max(1ll, (longest + kUnit - 1) / kUnit);
-    const long long units = most * d->sequences * c->kv_heads * r.row_blocks;
-    r.workgroups = static_cast<int>(std::min<long long>(units, static_cast<long long>(compute_units()) * decode::resident(r.dp, r.rt)));
-    r.join = most > 1;
+    const long long pairs = static_cast<long long>(d->sequences) * c->kv_heads * r.row_blocks;
+    const int resident = compute_units() * decode::resident(r.dp, r.rt);
+    r.few = std::max(1, resident / 4);
+    // Where the page table has little room for tokens, or there are pairs enough for the device, each goes to a workgroup as a
+    // whole and nothing is joined (heads of 128, 8 of the cache; us by rounds and whole: 1 sequence of 250 tokens 10.3 and 7.6, of 500 10.4
+    // and 9.2, of 1000 10.4 and 12; 32 sequences of 1000 20 and 15, of 2000 25 and 22; 64 of up to 4000 36 and 31, of up to 8192
+    // 69 and 71; 128 of up to 8192 131 and 128).
+    r.join = longest > std::max(512ll, std::min(8 * pairs, 8192ll));
+    r.workgroups = static_cast<int>(r.join ? std::min<long long>((longest + kRound - 1) / kRound * pairs, resident) : pairs);
     if (r.join) {
         const size_t slots = 2 * static_cast<size_t>(r.workgroups) * r.rt * 16;
         r.part_bytes = slots * c->head_dim * 4;
@@ -803,6 +840,8 @@ cfwd_status mx_cache_attention(const cfwd_mx_cache_attention_desc* d, const cfwd
     p.q_head_stride = d->q_head_stride;
     p.page = mx::divisor(c->page_size);
     p.per_group = mx::divisor(p.group);
+    p.whole = !plan.join;
+    p.few = plan.few;
     const bool one = c->page_size % 32 == 0;
     auto go = [&](auto whole, auto halves) {
         if (one) whole<<<plan.workgroups, 256, 0, st>>>(p);
