@@ -456,25 +456,39 @@ __global__ __launch_bounds__(64 * WAVES, SIMD_WAVES) void kernel(Params p) {
     }
 }
 
-// Joins the splits of rows (token, head) of q: 4 values a thread.
-__global__ __launch_bounds__(256) void join_kernel(Params p, Divisor across, uint32_t units) {
-    const uint32_t u = blockIdx.x * 256u + threadIdx.x;
-    if (u >= units) return;
-    const uint32_t row = divide(u, across), d = (u - row * across.d) * 4;
+// Joins the parts of rows (token, head) of q: 4 values a thread, eight parts or so, `strands` threads side by side for a row's
+// (1 query of 8 heads over 131072 keys, 256 parts: 58 us with one strand, 24 so; 256 of 32 heads over 16640, 8 parts: 87 with eight, 83 with one).
+__global__ __launch_bounds__(256) void join_kernel(Params p, int strands, int rows) {
+    __shared__ f32x4 area[256];
+    __shared__ float area_m[256], area_l[256];
+    const int across = p.dim / 4, in_row = across * strands, mine = threadIdx.x / in_row;
+    const int strand = threadIdx.x % in_row / across, d = threadIdx.x % across * 4;
+    const int row = blockIdx.x * (256 / in_row) + mine, token = row / p.heads;
     // rows before the first sequence and behind the last belong to none
-    const int token = row / p.heads;
-    if (token < p.q_starts[0] || token >= p.q_starts[p.sequences]) return;
+    const bool has = mine < 256 / in_row && row < rows && token >= p.q_starts[0] && token < p.q_starts[p.sequences];
     const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + static_cast<long long>(row) * p.splits;
     const float* part = p.part + static_cast<long long>(row) * p.splits * p.dim + d;
-    float m = kLow;
-    for (int s = 0; s < p.splits; ++s) m = fmaxf(m, ml[s].x);
     f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
-    float l = 0.0f;
+    float l = 0.0f, m = kLow;
+    auto add = [&](float m_of, float l_of, const f32x4& o) {
+        const float to = fmaxf(m, m_of), f = __builtin_amdgcn_exp2f(m - to), e = __builtin_amdgcn_exp2f(m_of - to);
+        m = to;
+        l = l * f + l_of * e;
+        sum = sum * f + o * e;
+    };
+    if (has) {
 #pragma unroll 4
-    for (int s = 0; s < p.splits; ++s) {
-        const float f = __builtin_amdgcn_exp2f(ml[s].x - m);
-        l += ml[s].y * f;
-        sum += *reinterpret_cast<const f32x4*>(part + static_cast<long long>(s) * p.dim) * f;
+        for (int s = strand; s < p.splits; s += strands)
+            add(ml[s].x, ml[s].y, *reinterpret_cast<const f32x4*>(part + static_cast<long long>(s) * p.dim));
+        area[threadIdx.x] = sum;
+        area_l[threadIdx.x] = l;
+        area_m[threadIdx.x] = m;
+    }
+    __syncthreads();
+    if (!has || strand != 0) return;
+    for (int s = 1; s < strands; ++s) {
+        const int at = threadIdx.x + s * across;
+        add(area_m[at], area_l[at], area[at]);
     }
     const float inverse = l == 0.0f ? 0.0f : 1.0f / l;
     uint2 y;
@@ -550,9 +564,9 @@ cfwd_status attention(const cfwd_attention_desc* d, const void* q, const void* k
     else go(fa::kernel<256, 16, 8, 4, 2, 3, 1>, 4);
     const cfwd_status e = check_hip(hipGetLastError(), "attention launch");
     if (e != CFWD_OK || plan.splits == 1) return e;
-    const long long units = d->q_tokens * d->q_heads * (d->head_dim / 4);  // split only where rows are few
-    fa::join_kernel<<<static_cast<unsigned>((units + 255) / 256), 256, 0, st>>>(p, mx::divisor(d->head_dim / 4),
-                                                                             static_cast<uint32_t>(units));
+    const int across = d->head_dim / 4, strands = std::min(256 / across, (plan.splits + 7) / 8), each = 256 / (across * strands);
+    const int rows = static_cast<int>(d->q_tokens * d->q_heads);  // split only where they are few
+    fa::join_kernel<<<(rows + each - 1) / each, 256, 0, st>>>(p, strands, rows);
     return check_hip(hipGetLastError(), "attention's joining launch");
 }
 

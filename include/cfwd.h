@@ -583,7 +583,9 @@ cfwd_status cfwd_mx_cache_attention(const cfwd_mx_cache_attention_desc *desc, co
  * on; a query that sees no key gives 0.  Rows of o behind the last sequence are
  * not written.  bf16; head_dim a multiple of 8 up to 256; q_heads a multiple of kv_heads; tensors 16-byte aligned, strides
  * multiples of 8 elements, k and v strides from head_dim to 2^24 (CFWD_ERR_UNSUPPORTED for others).  Products are exact and
- * summed in fp32, as are the softmax's sums; its weights are rounded to bf16 before the product with v. */
+ * summed in fp32, as are the softmax's sums; its weights are rounded to bf16 before the product with v.  They are taken
+ * relative to a number that the scores pass by at most a factor of 2^12, here as over the cache: values up to 2^90 or so
+ * leave the sums in fp32's range. */
 typedef struct {
     long long q_tokens, k_tokens;
     int sequences, q_heads, kv_heads, head_dim;

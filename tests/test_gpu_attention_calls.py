@@ -272,6 +272,18 @@ def test_few_queries_over_many_keys_that_are_not_finite():
         assert all(torch.equal(g, c) for g, c, s in zip(got, clean, sees) if not s)
 
 
+@pytest.mark.parametrize("nq,nk,h,kh,dim", [(1, 60000, 2, 1, 64), (3, 40000, 1, 1, 80), (2, 20000, 4, 2, 256), (1, 130000, 1, 1, 8)])
+def test_few_queries_over_very_many_keys(nq, nk, h, kh, dim):
+    """Hundreds of parts for a row, joined by several threads."""
+    torch = torch_cuda()
+    q, k, v = heads(torch, 1, nq + 2, h, dim), heads(torch, 2, nk, kh, dim), heads(torch, 3, nk, kh, dim)
+    out = torch.full_like(q, 7.0)
+    B.attention(q, k, v, ints(torch, [1, nq + 1]), ints(torch, [0, nk]), out=out)
+    want, bound = A.attend(np64(q[1:-1]), np64(k), np64(v), True, dim ** -0.5)
+    A.check(np64(out[1:-1]), want, bound)
+    assert bool((out[0] == 7).all()) and bool((out[-1] == 7).all())
+
+
 @pytest.mark.parametrize("dtype,tokens", [("bf16", 13000), ("f32", 6500)])
 def test_large_tensors_pass_the_caches_by(dtype, tokens):
     """Above the size from which loads pass the caches by, the same bits as from parts below it."""
