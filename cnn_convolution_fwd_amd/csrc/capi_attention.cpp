@@ -132,7 +132,7 @@ cfwd_status check_attention(const cfwd_attention_desc* d) {
         return set_error(CFWD_ERR_UNSUPPORTED, "attention needs a head_dim that is a multiple of 8, at most 256");
     if (d->q_tokens >= (1ll << 31) / d->q_heads || d->k_tokens >= (1ll << 31) - 4096)
         return set_error(CFWD_ERR_UNSUPPORTED, "q_tokens times q_heads, and k_tokens, must stay below 2^31");
-    if ((d->q_tokens * (d->q_heads / d->kv_heads) / 128 + std::min<long long>(d->sequences, d->q_tokens) + 1) * d->kv_heads >= (1ll << 31))
+    if ((d->q_tokens * (d->q_heads / d->kv_heads) / 128 + d->sequences + 1) * d->kv_heads >= (1ll << 31))
         return set_error(CFWD_ERR_UNSUPPORTED, "too many tiles for one launch");
     const struct { long long rows; int heads; long long stride, head; } t[] = {
         {d->q_tokens, d->q_heads, d->q_stride, d->q_head_stride}, {d->k_tokens, d->kv_heads, d->k_stride, d->k_head_stride},

@@ -89,9 +89,13 @@ __global__ __launch_bounds__(256) void read_kernel(Params p, const int32_t* __re
     const int lane = threadIdx.x & 63;
     for (int i = threadIdx.x >> 6; i < tokens; i += 4) {
         const long long t = t0 + i;
-        int seq = 0;  // sequences that end at or before t
-        for (int s = 0; s < p.sequences; s += 64)
-            seq += __popcll(__ballot(s + lane < p.sequences && starts[min(s + lane, p.sequences - 1) + 1] <= t));
+        // sequences that end at or before t, by looking at 64 evenly spaced, and at 64 between two of those, ...
+        int seq = 0;
+        for (int step, left = p.sequences; left > 0; left = step == 1 ? 0 : min(step, p.sequences - seq)) {
+            step = (left + 63) / 64;
+            const int s = (lane + 1) * step;
+            seq += __popcll(__ballot(s <= left && starts[seq + s] <= t)) * step;
+        }
         long long row = -1;
         if (seq < p.sequences) {
             const long long at = t - starts[seq];

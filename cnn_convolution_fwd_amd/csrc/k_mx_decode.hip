@@ -522,18 +522,21 @@ __global__ __launch_bounds__(256, resident(DP, RT)) void kernel(Params p) {
         unit = rounds_of(length);
     } else {
         // the units of all sequences, then the sequence in which the first unit of this workgroup lies
-        int its, rounds = rounds_at(p, 0, lane, &its), total = __builtin_amdgcn_readlane(wave_scan(rounds), 63);
+        int its, rounds = rounds_at(p, 0, lane, &its), sum = rounds;
+#pragma unroll 4
         for (int s = 64; s < p.sequences; s += 64) {
             int unused;
-            total += __builtin_amdgcn_readlane(wave_scan(rounds_at(p, s, lane, &unused)), 63);
+            sum += rounds_at(p, s, lane, &unused);
         }
-        unit = unit_of(p, total);
+        unit = unit_of(p, __builtin_amdgcn_readlane(wave_scan(sum), 63));
         int mine = (rounds + unit - 1) / unit, upto = wave_scan(mine);
-        total = __builtin_amdgcn_readlane(upto, 63);
+        sum = mine;
+#pragma unroll 4
         for (int s = 64; s < p.sequences; s += 64) {
             int unused;
-            total += __builtin_amdgcn_readlane(wave_scan((rounds_at(p, s, lane, &unused) + unit - 1) / unit), 63);
+            sum += (rounds_at(p, s, lane, &unused) + unit - 1) / unit;
         }
+        const int total = __builtin_amdgcn_readlane(wave_scan(sum), 63);
         shares = shares_of(p, total);
         if (u >= shares.workgroups) return;
         end = shares.begin(u + 1);

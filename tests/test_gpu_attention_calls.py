@@ -209,6 +209,55 @@ def test_many_sequences():
         A.check(np64(packed[a[i]:a[i + 1]]), want, bound)
 
 
+@pytest.mark.parametrize("n,most", [(65, 300), (128, 200), (1000, 5), (5000, 3), (4097, 2)])
+@pytest.mark.parametrize("h", [1, 6])
+def test_very_many_packed_sequences(n, most, h):
+    """Every sequence's rows as they are alone; many empty ones, at both ends as well."""
+    torch = torch_cuda()
+    rng = np.random.default_rng(n)
+    lengths = rng.integers(0, most + 1, n) * (rng.random(n) < 0.7)
+    if n != 128:
+        lengths[:3], lengths[-70:] = 0, lengths[-70:] * (n != 1000)
+    else:
+        lengths[:] = 128  # whole tiles
+    a = np.concatenate([[0], np.cumsum(lengths)]) + 2
+    total = int(a[-1]) + 3
+    qkv = heads(torch, n, total, h + 2, 32)
+    out = torch.full((total, h, 32), 7.0, dtype=torch.bfloat16, device="cuda")
+    B.attention(qkv[:, :h], qkv[:, h:h + 1], qkv[:, h + 1:], ints(torch, a), causal=n % 2 == 0, out=out)
+    assert bool((out[:2] == 7).all()) and bool((out[-3:] == 7).all())
+    few = [int(i) for i in rng.choice(np.flatnonzero(lengths), 40)] + [int(np.flatnonzero(lengths)[i]) for i in (0, -1)]
+    for i in few:
+        s = slice(int(a[i]), int(a[i + 1]))
+        x = np64(qkv[s])
+        want, bound = A.attend(x[:, :h], x[:, h:h + 1], x[:, h + 1:], n % 2 == 0, 32 ** -0.5)
+        A.check(np64(out[s]), want, bound)
+    # all of them, by parts of 64 sequences
+    for i in range(0, n, 64):
+        j = min(n, i + 64)
+        s = slice(int(a[i]), int(a[j]))
+        part = B.attention(qkv[s, :h], qkv[s, h:h + 1], qkv[s, h + 1:], ints(torch, a[i:j + 1] - a[i]), causal=n % 2 == 0)
+        assert torch.equal(part, out[s])
+
+
+@pytest.mark.parametrize("n", [64, 65, 1000, 4097])
+def test_very_many_sequences_read(n):
+    torch = torch_cuda()
+    rng = np.random.default_rng(n)
+    lengths = rng.integers(0, 4, n) * (rng.random(n) < 0.7)
+    lengths[0], lengths[-1] = 0, 2 * (n % 2)
+    cache = B.mx_cache(n, 3, 1, 32)
+    kv = heads(torch, n, 3 * n, 2, 32, "f32")
+    B.mx_cache_write(kv[:, :1], kv[:, 1:], cache, torch.arange(3 * n, device="cuda"))
+    pages = rng.permutation(n)
+    a = np.concatenate([[0], np.cumsum(lengths)])
+    rows = np.concatenate([pages[i] * 3 + np.arange(m) for i, m in enumerate(lengths)])
+    got = B.mx_cache_read(cache, ints(torch, pages[:, None]), ints(torch, a), int(a[-1]), dtype="f32")
+    for t, out in zip(cache, got):
+        want = B.mx_dequantize(t, dtype="f32").view(3 * n, 1, 32)[torch.as_tensor(rows, device="cuda")]
+        assert torch.equal(out, want)
+
+
 def test_shared_pages():
     """Sequences that begin with the same pages, and one page twice in a row."""
     torch = torch_cuda()
