@@ -26,6 +26,9 @@
 // Two waves a SIMD (three for heads of 64) fill what is left.
 //
 // Few rows over many keys are split over the keys; a second launch joins the parts.
+//
+// Bound by the matrix cores for heads of 128 (16384 tokens, 32 heads over 8, causal: 2.0 ms, 1.1 PFLOP/s, busy 63% of the cycles; the
+// matrix instructions alone take 1.3 ms) and by vector instructions for heads of 64 (32 images of 784 tokens, 16 heads: 127 us).
 #include "attention.h"
 #include "mx.h"
 

